@@ -870,10 +870,12 @@ __device__ __forceinline__ void decode_chunk(const GroupEntry &g, const Smem &s,
                     ld[k].step(pk, SLOW && refill_each, s.slim, s.soffs, s.ssyms, d.max_len, status);
                     ld[k].step(pk, true, s.slim, s.soffs, s.ssyms, d.max_len, status);
                 }
-                // a partial last run: its slot holds the codes after every lookup
-                if (tail && full_runs < te)
+                // a partial last run
+                if (tail && full_runs < te) {
                     while (ld[k].runs() == full_runs && ((ld[k].C >> kPbShift) & 0xFFu) < tail * BITS)
                         ld[k].step(pk, true, s.slim, s.soffs, s.ssyms, d.max_len, status);
+                    if (ld[k].runs() == full_runs) ld[k].store_pending();
+                }
             }
             __syncwarp();
             emit_ragged<BITS, OUT, LANES>(g, s, ost, first, nc, tb, te);

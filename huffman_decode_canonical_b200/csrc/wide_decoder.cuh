@@ -174,6 +174,16 @@ struct WideDecoder {
             : "memory");
     }
 
+    // The pending codes into the current run's slot.  A lookup that completes a run may bring
+    // codes of the next one, whose slot only the next lookup would store: a partial last run
+    // that came whole that way has no next lookup.
+    __device__ __forceinline__ void store_pending() const {
+        if (BITS == 4)
+            asm volatile("st.shared.u32 [%0], %1;" ::"r"(osta), "r"(p0) : "memory");
+        else
+            asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(osta), "r"(p0), "r"(p1) : "memory");
+    }
+
     __device__ __forceinline__ uint2 entry(const Pipes &k) const {
         return lds64(imad(imulhi(hi, k.two12), k.eight, tab));  // table[window >> 52]
     }
