@@ -18,7 +18,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from typing import List, Optional, Sequence
+from typing import List, NamedTuple, Optional, Sequence, Union
 
 import numpy as np
 import torch
@@ -61,7 +61,8 @@ EXPORTS = ["entro_encode", "entro_blob_from_bytes", "entro_blob_bytes", "entro_b
            "entro_device_bytes", "entro_upload", "entro_tensor_free", "entro_decode_codes",
            "entro_decode_dequant_bf16", "entro_decode_gemv", "entro_group_table_bytes", "entro_group_prepare",
            "entro_group_launch", "entro_group_free", "entro_strerror", "entro_version", "entro_last_cuda_error",
-           "entro_decode_gemv_group_static", "entro_set_overlap", "entro_test_stall_tables"]
+           "entro_decode_gemv_group_static", "entro_set_overlap", "entro_test_stall_tables",
+           "entro_quantize_tokens", "entro_unpack_codes", "entro_matmul_i8"]
 
 
 def _load() -> ctypes.CDLL:
@@ -70,6 +71,7 @@ def _load() -> ctypes.CDLL:
                           "(there is no CPU fallback)")
     lib = ctypes.CDLL(LIB_PATH)
     P, I32, I64, U64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_uint64
+    F32 = ctypes.c_float
     PP = ctypes.POINTER(ctypes.c_void_p)
     sig = {
         "entro_encode": ([P, I64, I64, ctypes.POINTER(_Opts), PP], I32),
@@ -93,6 +95,9 @@ def _load() -> ctypes.CDLL:
         "entro_decode_gemv_group_static": ([P, P, P, I32, I32, P, P], I32),
         "entro_set_overlap": ([I32], I32),
         "entro_test_stall_tables": ([ctypes.c_uint32], ctypes.c_uint32),
+        "entro_quantize_tokens": ([P, I32, I64, I64, I64, P, I64, P, P, P], I32),
+        "entro_unpack_codes": ([P, I32, I64, I64, P, I64, P], I32),
+        "entro_matmul_i8": ([P, I64, P, P, I64, P, I32, I64, I64, I64, P, F32, P, I32, P, I32, I64, P, P], I32),
     }
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
@@ -253,6 +258,28 @@ class DeviceTensor:
                "entro_decode_gemv")
         return y
 
+    def matmul(self, x: torch.Tensor, out: Optional[torch.Tensor] = None, out_dtype: torch.dtype = torch.bfloat16,
+               status: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+        """x @ w.T for any number of tokens (a prompt): x bf16 or fp16 [tokens, cols], or `QuantTokens` that
+        several projections share.  The codes are decoded into a buffer of their own for the call, the tokens
+        quantized to 8 bits each with its scale, and multiplied in integers (`matmul_i8`)."""
+        if not isinstance(x, QuantTokens) and (x.dim() != 2 or x.shape[1] != self.cols):
+            raise ValueError("x must be a [tokens, cols] tensor")
+        with _on(self.device, stream) as s:
+            codes = self.empty_codes()
+            _check(_lib.entro_decode_codes(self._h, _dptr(codes), _dptr(status), s), "entro_decode_codes")
+            if self.bits == 8 and self.cols % 16 == 0:
+                w = codes[:self.n].view(self.rows, self.cols)
+            else:
+                pitch = _pitch(self.cols)
+                w = torch.empty((self.rows, pitch), dtype=torch.uint8, device=self.device)
+                _check(_lib.entro_unpack_codes(_dptr(codes), self.bits, self.rows, self.cols, _dptr(w), pitch, s),
+                       "entro_unpack_codes")
+                w = w[:, :self.cols]
+            xq = x if isinstance(x, QuantTokens) else quantize_tokens(x, stream=stream)
+            return matmul_i8(xq, w, self.info["scale"], self.info["zero"], out=out, out_dtype=out_dtype, status=status,
+                             stream=stream)
+
     def close(self):
         if getattr(self, "_h", None) and _lib is not None:
             _lib.entro_tensor_free(self._h)
@@ -323,6 +350,122 @@ def decode_gemv_group_static(tensors: Sequence[DeviceTensor], xs: Sequence[torch
                                                _stream_ptr(stream)), "entro_decode_gemv_group_static")
 
 
+# ------------------------------------------------------------------ around the coded weights
+
+F32, BF16, F16, U8, S8 = range(5)
+_TYPES = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16, torch.uint8: U8, torch.int8: S8}
+
+
+class _on:
+    """The tensors' device as the current one, and new buffers from the pool of the stream that is launched on."""
+
+    def __init__(self, device: torch.device, stream: Optional[torch.cuda.Stream]):
+        self.guards = []
+        if stream is not None:
+            if stream.device != device:
+                raise ValueError("the stream belongs to another device than the tensors")
+            self.guards.append(torch.cuda.stream(stream))
+        elif device.index != torch.cuda.current_device():
+            self.guards.append(torch.cuda.device(device))
+        self.device = device
+
+    def __enter__(self) -> int:
+        for g in self.guards:
+            g.__enter__()
+        return torch.cuda.current_stream(self.device).cuda_stream
+
+    def __exit__(self, *e):
+        for g in reversed(self.guards):
+            g.__exit__(*e)
+
+
+def _inputs(device: torch.device, **tensors):
+    """Refuses what the kernels must not be given: tensors of other devices, or ones that ask for gradients."""
+    if device.type != "cuda":
+        raise ValueError("expected CUDA tensors")
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if t.device != device:
+            raise ValueError(f"{name} is on {t.device}, not on {device}")
+        if t.requires_grad and torch.is_grad_enabled():
+            raise ValueError(f"{name} requires a gradient: this call has none (use torch.no_grad())")
+
+
+def _pitch(cols: int) -> int:
+    return (cols + 15) // 16 * 16
+
+
+class QuantTokens(NamedTuple):
+    """Activations in 8 bits: codes int8 [tokens, cols] (rows a multiple of 16 bytes apart), scale fp32 [tokens], sum
+    int32 [tokens] (of a token's codes)."""
+    codes: torch.Tensor
+    scale: torch.Tensor
+    sum: torch.Tensor
+
+
+def quantize_tokens(x: torch.Tensor, stream: Optional[torch.cuda.Stream] = None) -> QuantTokens:
+    """bf16 or fp16 [tokens, cols] (any row stride) to codes 127 x / max|x| of each token, with scale max|x| / 127."""
+    if x.dtype not in (torch.bfloat16, torch.float16) or x.dim() != 2 or x.shape[1] < 1 or x.stride(1) != 1:
+        raise ValueError("x must be a bf16 or fp16 [tokens, cols] tensor with adjacent columns")
+    _inputs(x.device, x=x)
+    tokens, cols = x.shape
+    pitch = _pitch(cols)
+    with _on(x.device, stream) as s:
+        codes = torch.empty((tokens, pitch), dtype=torch.int8, device=x.device)
+        scale = torch.empty(tokens, dtype=torch.float32, device=x.device)
+        total = torch.empty(tokens, dtype=torch.int32, device=x.device)
+        _check(_lib.entro_quantize_tokens(x.data_ptr(), _TYPES[x.dtype], tokens, cols, x.stride(0) if tokens > 1 else pitch,
+                                          codes.data_ptr(), pitch, scale.data_ptr(), total.data_ptr(), s),
+               "entro_quantize_tokens")
+    return QuantTokens(codes if pitch == cols else codes[:, :cols], scale, total)
+
+
+def matmul_i8(x: QuantTokens, w: torch.Tensor, w_scale: Union[float, torch.Tensor], w_zero: Union[None, int, torch.Tensor] = None,
+              out: Optional[torch.Tensor] = None, out_dtype: torch.dtype = torch.bfloat16,
+              status: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """y[t, n] = x.scale[t] * w_scale[n] * sum_k x.codes[t, k] * (w[n, k] - w_zero[n]).
+
+    w uint8 or int8 [rows, cols], adjacent columns, rows a multiple of 16 bytes apart; w_scale a number or fp32 [rows];
+    w_zero a whole number, int32 [rows] or None (0).  out: fp32, bf16 or fp16 [tokens, rows] with adjacent columns."""
+    q = x.codes
+    if w.dtype not in (torch.uint8, torch.int8) or w.dim() != 2 or w.shape[1] < 1 or w.stride(1) != 1:
+        raise ValueError("w must be a uint8 or int8 [rows, cols] tensor with adjacent columns")
+    rows, cols = w.shape
+    tokens = q.shape[0] if q.dim() == 2 else -1
+    if q.dtype != torch.int8 or q.dim() != 2 or q.shape[1] != cols or q.stride(1) != 1:
+        raise ValueError("x.codes must be an int8 [tokens, cols] tensor with adjacent columns")
+    for t, dtype, name in ((x.scale, torch.float32, "x.scale"), (x.sum, torch.int32, "x.sum")):
+        if t.dtype != dtype or t.shape != (tokens,) or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous {dtype} [tokens] tensor")
+    ws, wz = torch.is_tensor(w_scale), torch.is_tensor(w_zero)
+    if ws and (w_scale.dtype != torch.float32 or w_scale.shape != (rows,) or not w_scale.is_contiguous()):
+        raise ValueError("w_scale must be a number or a contiguous fp32 [rows] tensor")
+    if wz and (w_zero.dtype != torch.int32 or w_zero.shape != (rows,) or not w_zero.is_contiguous()):
+        raise ValueError("w_zero must be a whole number or a contiguous int32 [rows] tensor")
+    if not wz and w_zero is not None and not -2 ** 31 <= w_zero < 2 ** 31:
+        raise ValueError("w_zero must fit 32 bits")
+    _inputs(w.device, w=w, codes=q, scale=x.scale, sum=x.sum, w_scale=w_scale if ws else None, w_zero=w_zero if wz else None,
+            out=out, status=status)
+    # a single row's stride says nothing
+    ldq, ldw = (q.stride(0) if tokens > 1 else _pitch(cols)), (w.stride(0) if rows > 1 else _pitch(cols))
+    if ldq % 16 or ldw % 16 or q.data_ptr() % 16 or w.data_ptr() % 16:
+        raise ValueError("x.codes and w must begin on 16 bytes, their rows a multiple of 16 bytes apart")
+    with _on(w.device, stream) as s:
+        if out is None:
+            out = torch.empty((tokens, rows), dtype=out_dtype, device=w.device)
+        elif out.shape != (tokens, rows) or (rows > 1 and out.stride(1) != 1) or (tokens > 1 and out.stride(0) < rows):
+            raise ValueError("out must be a [tokens, rows] tensor with adjacent columns")
+        if out.dtype not in (torch.float32, torch.bfloat16, torch.float16):
+            raise ValueError("out must be fp32, bf16 or fp16")
+        _check(_lib.entro_matmul_i8(q.data_ptr(), ldq, x.scale.data_ptr(), x.sum.data_ptr(), tokens, w.data_ptr(), _TYPES[w.dtype],
+                                    ldw, rows, cols, w_scale.data_ptr() if ws else None, 0.0 if ws else float(w_scale),
+                                    w_zero.data_ptr() if wz else None, 0 if wz or w_zero is None else int(w_zero),
+                                    out.data_ptr(), _TYPES[out.dtype], out.stride(0) if tokens > 1 else rows,
+                                    _dptr(status), s), "entro_matmul_i8")
+    return out
+
+
 def test_stall_tables(extra_bytes: int) -> int:
     """Test hook for the bounded waits: later launches wait for `extra_bytes` of table copy that
     never arrive, so each gives up after about a second with E_TIMEOUT in the status word.
@@ -344,7 +487,7 @@ def set_overlap(enable: bool) -> bool:
 
 
 __all__ = ["Blob", "DeviceTensor", "Group", "EntroError", "encode", "upload", "lib", "version", "set_overlap", "EXPORTS",
-           "decode_gemv_group_static", "STATIC_GROUP_MAX",
+           "decode_gemv_group_static", "STATIC_GROUP_MAX", "QuantTokens", "quantize_tokens", "matmul_i8",
            "test_stall_tables", "QUANT_AUTO", "QUANT_UNSIGNED", "QUANT_ASYM", "FORMAT_SINGLE", "FORMAT_LANES", "FORMAT_ROWS_CO",
            "FORMAT_ROWS", "GROUP_GEMV",
            "GROUP_BF16", "SCHEME_UNSIGNED", "SCHEME_ASYM"]

@@ -18,7 +18,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libentro.so")
-SOURCES = [os.path.join(CSRC, "decode.cu"), os.path.join(CSRC, "encoder.cpp")]
+OBJECTS = os.path.join(HERE, "_build")
+SOURCES = [os.path.join(CSRC, f) for f in ("decode.cu", "product.cu", "encoder.cpp", "launch.cpp")]
 HEADERS = sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".h", ".cuh"))) + [
     os.path.join(ROOT, "include", "entro.h")]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
@@ -31,16 +32,41 @@ def _stale() -> bool:
     return any(os.path.getmtime(p) > t for p in SOURCES + HEADERS)
 
 
+def _object(src: str) -> str:
+    return os.path.join(OBJECTS, os.path.basename(src) + ".o")
+
+
+def _outdated(src: str) -> bool:
+    obj = _object(src)
+    return not os.path.exists(obj) or any(os.path.getmtime(p) > os.path.getmtime(obj) for p in [src] + HEADERS)
+
+
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     if not force and not _stale():
         return LIB
-    tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [NVCC, "-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo", "-O3", "-std=c++17",
-           "-shared", "-Xcompiler", "-fPIC,-pthread,-ffp-contract=off,-fvisibility=hidden",
-           "-I", os.path.join(ROOT, "include"), "-I", CSRC, "-o", tmp] + SOURCES + ["-lpthread"]
+    os.makedirs(OBJECTS, exist_ok=True)
+    flags = ["-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo", "-O3", "-std=c++17",
+             "-Xcompiler", "-fPIC,-pthread,-ffp-contract=off,-fvisibility=hidden",
+             "-I", os.path.join(ROOT, "include"), "-I", CSRC]
     if verbose_ptxas:
-        cmd[1:1] = ["-Xptxas", "-v"]
-    subprocess.check_call(cmd)
+        flags = ["-Xptxas", "-v"] + flags
+    running = []
+    for src in SOURCES:  # the sources side by side
+        if force or _outdated(src):
+            tmp = _object(src) + f".tmp{os.getpid()}"
+            cmd = [NVCC] + flags + ["-c", "-o", tmp, src]
+            running.append((cmd, tmp, _object(src), subprocess.Popen(cmd)))
+    bad = None
+    for cmd, tmp, obj, p in running:
+        if p.wait() != 0:
+            bad = bad or (p.returncode, cmd)
+        else:
+            os.replace(tmp, obj)
+    if bad:
+        raise subprocess.CalledProcessError(*bad)
+    tmp = LIB + f".tmp{os.getpid()}"
+    subprocess.check_call([NVCC, "-gencode", "arch=compute_100a,code=sm_100a", "-shared", "-o", tmp]
+                          + [_object(s) for s in SOURCES] + ["-lpthread"])
     os.replace(tmp, LIB)
     return LIB
 

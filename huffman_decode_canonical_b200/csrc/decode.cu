@@ -50,6 +50,7 @@
 #include "blob_format.h"
 #include "entro.h"
 #include "entro_internal.h"
+#include "launch.h"
 
 namespace entro {
 
@@ -1736,21 +1737,16 @@ __global__ void __launch_bounds__(kSegThreads) segment_kernel(const __grid_const
 // Message of the last CUDA runtime error the library saw on this host thread.
 static thread_local char g_cuda_msg[160] = "";
 
-static int cuda_fail(cudaError_t e, const char *where) {
+int cuda_fail(cudaError_t e, const char *where) {
     snprintf(g_cuda_msg, sizeof(g_cuda_msg), "%s: %s (%d)", where, cudaGetErrorString(e), (int)e);
     return ENTRO_E_CUDA;
 }
-
-struct DeviceInfo {
-    int sms = 0;
-    int smem_optin = 0;
-};
 
 static std::mutex g_mu;
 constexpr int kMaxDevices = 64;
 static DeviceInfo g_dev[kMaxDevices];
 
-static int device_info(int dev, DeviceInfo *out) {
+int device_info(int dev, DeviceInfo *out) {
     std::lock_guard<std::mutex> lk(g_mu);
     if (dev < 0 || dev >= kMaxDevices) return ENTRO_E_LIMIT;
     DeviceInfo &di = g_dev[dev];
@@ -2054,6 +2050,7 @@ static int kernel_config(const void *fn, int device, int threads, size_t bytes, 
 static std::atomic<int> g_overlap{0};
 // Bounded-wait test hook: bytes every launch adds to its table barrier that never arrive.
 static std::atomic<uint32_t> g_tx_extra{0};
+uint32_t test_tx_extra() { return g_tx_extra.load(std::memory_order_relaxed); }
 
 // overlap_ok: the kernel fills each SM with one CTA (the next launch's CTAs
 // cannot move in before this one's leave).  Kernels with several CTAs per SM

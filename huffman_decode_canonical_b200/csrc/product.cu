@@ -1,0 +1,646 @@
+// product.cu -- products of more activation rows than the fused GEMV takes:
+// activations quantized to 8 bits per token, times 8-bit weight codes on the
+// integer tensor cores (tcgen05, kind::i8), with a scale for each token and
+// channel.
+//
+//   a_t = max_k |x[t, k]|,  q[t, k] = rint(127 x[t, k] / a_t),  s_t = a_t / 127
+//   y[t, n] = s_t w_n (sum_k q[t, k] c[n, k] - z_n sum_k q[t, k])
+//
+// The codes c are what entro_decode_codes writes for an 8-bit tensor (unsigned,
+// with the tensor's zero point z and scale w) or any other 8-bit weights.  The
+// sums are exact 32-bit integers, so a result does not depend on how the work
+// is split.  In the MMA the weights are operand A (their rows are the TMEM
+// lanes) and the tokens operand B, so few tokens make a narrow tile instead of
+// a padded one, and a warp's 32 outputs of one token are adjacent in memory.
+#include <algorithm>
+#include <cstring>
+
+#include "launch.h"
+#include "sm100.cuh"
+
+namespace entro {
+using namespace sm100;
+
+// ------------------------------------------------------------------ tokens to 8 bits
+
+// 127 x / amax to the nearest whole number, ties to even, exactly: 127 x is
+// exact (at most 18 bits), its product with the rounded reciprocal is off by
+// less than 2^-23 of itself, and a quotient of two numbers of at most 11 bits
+// that is no tie lies at least 2^-19 of itself away from one.  So rounding the
+// product to 20 bits (a split by 2^4 + 1) restores ties and moves nothing else
+// across one.
+__device__ __forceinline__ int code_of(float x127, float rcp) {
+    const float t = __fmul_rn(x127, rcp), c = __fmul_rn(t, 17.0f);
+    return __float2int_rn(__fsub_rn(c, __fsub_rn(c, t)));
+}
+
+struct QuantArgs {
+    const uint16_t *x;
+    int8_t *q;
+    float *scale;
+    int32_t *sum;
+    int64_t tokens, cols, ldx, ldq;
+};
+
+constexpr int kQuantThreads = 256;
+
+// One CTA a token.  The row stays in registers between its two uses (VECS
+// 16-byte loads a thread; 0: rows too long or too unaligned for that, read twice
+// element by element).  Bound by memory: 3 bytes an element.
+template <typename T, int VECS>
+__global__ void __launch_bounds__(kQuantThreads) quantize_kernel(const QuantArgs a) {
+    __shared__ uint32_t red_max[kQuantThreads / 32];
+    __shared__ int red_sum[kQuantThreads / 32];
+    dependents_may_launch();
+    const int tid = threadIdx.x;
+    const int64_t t = blockIdx.x;
+    const uint16_t *row = a.x + t * a.ldx;
+    uint4 v[VECS ? VECS : 1];
+    uint32_t m = 0;  // of the halves without their signs: ordered as their values are, infinities and NaN at the top
+    if (VECS) {
+#pragma unroll
+        for (int i = 0; i < VECS; i++) {
+            const int64_t k = (static_cast<int64_t>(i) * kQuantThreads + tid) * 8;
+            v[i] = make_uint4(0, 0, 0, 0);
+            if (k + 8 <= a.cols) {
+                v[i] = __ldg(reinterpret_cast<const uint4 *>(row + k));
+            } else if (k < a.cols) {
+                uint16_t e[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+                for (int j = 0; j < 8 && k + j < a.cols; j++) e[j] = row[k + j];
+                std::memcpy(&v[i], e, 16);
+            }
+            m = __vmaxu2(m, __vmaxu2(__vmaxu2(v[i].x & 0x7FFF7FFFu, v[i].y & 0x7FFF7FFFu),
+                                     __vmaxu2(v[i].z & 0x7FFF7FFFu, v[i].w & 0x7FFF7FFFu)));
+        }
+    } else {
+        for (int64_t k = tid; k < a.cols; k += kQuantThreads) m = max(m, static_cast<uint32_t>(row[k] & 0x7FFF));
+    }
+    m = max(m & 0xFFFF, m >> 16);
+    m = __reduce_max_sync(~0u, m);
+    if (tid % 32 == 0) red_max[tid / 32] = m;
+    __syncthreads();
+    m = 0;
+    for (int w = 0; w < kQuantThreads / 32; w++) m = max(m, red_max[w]);
+    const bool finite = m < (Half<T>::kExp & 0xFFFF);
+    const float amax = Half<T>::widen(m).x;
+    // keep products and reciprocal inside the normal range (powers of two: exact)
+    const float pre = amax > 0x1p60f ? 0x1p-64f : amax < 0x1p-60f ? 0x1p64f : 1.0f;
+    const float rcp = finite && amax > 0 ? __frcp_rn(amax * pre) : 0.0f;
+    const float by = finite ? 127.0f * pre : 0.0f;
+    int sum = 0;
+    auto code = [&](float x) { return finite ? code_of(x * by, rcp) : 0; };
+    if (VECS) {
+#pragma unroll
+        for (int i = 0; i < VECS; i++) {
+            const int64_t k = (static_cast<int64_t>(i) * kQuantThreads + tid) * 8;
+            if (k >= a.cols) break;
+            const uint32_t e[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+            uint32_t o[2];
+#pragma unroll
+            for (int j = 0; j < 2; j++) {
+                const float2 p = Half<T>::widen(e[2 * j]), r = Half<T>::widen(e[2 * j + 1]);
+                const uint32_t lo = __byte_perm(code(p.x), code(p.y), 0x0040), hi = __byte_perm(code(r.x), code(r.y), 0x0040);
+                o[j] = __byte_perm(lo, hi, 0x5410);
+                sum = __dp4a(static_cast<int>(o[j]), 0x01010101, sum);
+            }
+            // the row pitch is a multiple of 16 bytes: the last vector's zeros fall inside it
+            *reinterpret_cast<uint2 *>(a.q + t * a.ldq + k) = make_uint2(o[0], o[1]);
+        }
+    } else {
+        for (int64_t k = tid; k < a.cols; k += kQuantThreads) {
+            const int c = code(Half<T>::widen(row[k]).x);
+            a.q[t * a.ldq + k] = static_cast<int8_t>(c);
+            sum += c;
+        }
+    }
+    sum = __reduce_add_sync(~0u, sum);
+    if (tid % 32 == 0) red_sum[tid / 32] = sum;
+    __syncthreads();
+    if (tid == 0) {
+        sum = 0;
+        for (int w = 0; w < kQuantThreads / 32; w++) sum += red_sum[w];
+        a.sum[t] = sum;
+        a.scale[t] = finite ? __fdiv_rn(amax, 127.0f) : __int_as_float(0x7FC00000);
+    }
+}
+
+// ------------------------------------------------------------------ codes to a byte each
+
+// Packed 4-bit codes, or 8-bit ones in rows of any length, to a byte each in
+// rows of `ld` bytes (a multiple of 16, which the product's copies need).
+__global__ void __launch_bounds__(256) unpack_kernel(const uint8_t *codes, int bits, int64_t rows, int64_t cols, uint8_t *out,
+                                                     int64_t ld) {
+    const int64_t words = ld / 16, total = rows * words;
+    for (int64_t i = blockIdx.x * 256LL + threadIdx.x; i < total; i += gridDim.x * 256LL) {
+        const int64_t r = i / words, k0 = i % words * 16, first = r * cols + k0;
+        uint32_t o[4] = {0, 0, 0, 0};
+        if (bits == 4 && first % 2 == 0 && k0 + 16 <= cols && first % 16 == 0) {
+            const uint2 v = __ldg(reinterpret_cast<const uint2 *>(codes + first / 2));
+            const uint32_t w[2] = {v.x, v.y};
+#pragma unroll
+            for (int j = 0; j < 2; j++) {
+                const uint32_t lo = w[j] & 0x0F0F0F0Fu, hi = (w[j] >> 4) & 0x0F0F0F0Fu;
+                o[2 * j] = __byte_perm(lo, hi, 0x5140);
+                o[2 * j + 1] = __byte_perm(lo, hi, 0x7362);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 16; j++) {
+                if (k0 + j >= cols) break;
+                const int64_t s = first + j;
+                const uint32_t c = bits == 4 ? (codes[s / 2] >> (s % 2 * 4)) & 15u : codes[s];
+                o[j / 4] |= c << (j % 4 * 8);
+            }
+        }
+        *reinterpret_cast<uint4 *>(out + r * ld + k0) = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+}
+
+// ------------------------------------------------------------------ the product
+
+enum OutType { OUT_F32 = 0, OUT_BF16T = 1, OUT_F16T = 2 };
+
+struct ProductArgs {
+    const float *x_scale;
+    const int32_t *x_sum;
+    const float *w_scale;   // per channel, or null: w_scale_all
+    const int32_t *w_zero;  // per channel, or null: w_zero_all
+    float w_scale_all;
+    int32_t w_zero_all;
+    void *y;
+    int64_t ldy;
+    int32_t *status;
+    int tokens, rows, cols;
+    int bn;          // tokens of a tile
+    int chunks;      // 128-byte steps over cols
+    int stages;
+    int row_tiles, token_tiles;
+    uint32_t idesc, tmem_cols, tx_extra;
+};
+
+__device__ __forceinline__ void store_out(void *y, int64_t at, float v, int type) {
+    if (type == OUT_F32) static_cast<float *>(y)[at] = v;
+    else if (type == OUT_BF16T) static_cast<__nv_bfloat16 *>(y)[at] = __float2bfloat16_rn(v);
+    else static_cast<__half *>(y)[at] = __float2half_rn(v);
+}
+
+// One channel's part of the epilogue.
+struct Channel {
+    float scale;
+    int32_t zero;
+    bool wide;  // the zero point is outside the codes' range: its product may pass 32 bits
+
+    __device__ __forceinline__ void load(const ProductArgs &a, int n) {
+        scale = n < a.rows ? (a.w_scale ? a.w_scale[n] : a.w_scale_all) : 0.0f;
+        zero = n < a.rows ? (a.w_zero ? a.w_zero[n] : a.w_zero_all) : 0;
+        wide = zero < -256 || zero > 256;
+    }
+    // acc - zero * sum: in the codes' range the difference is a sum of cols products of at most 127 * 511,
+    // below 2^31 for cols up to 32768; past that, or for other zero points, it is taken in 64 bits
+    __device__ __forceinline__ float value(int32_t acc, int32_t sum, float x_scale, bool in64) const {
+        const float v = in64 ? static_cast<float>(static_cast<long long>(acc) - static_cast<long long>(zero) * sum)
+                             : static_cast<float>(acc - zero * sum);
+        return v * (x_scale * scale);
+    }
+};
+
+constexpr int kChunkBytes = 128;                 // k bytes of a stage: one swizzle row
+constexpr int kTileRows = 128;                   // weight rows of a CTA's tile
+constexpr int kABytes = kTileRows * kChunkBytes;
+
+// Few tokens: one tile of 128 weight rows by all tokens (up to 256) a cluster,
+// whose CTAs share the k range; the partial sums meet in shared memory over the
+// cluster (each CTA finishes a share of the tokens).  Bound by reading the
+// weights once; the split is what lets a projection of 16 row tiles use all SMs.
+template <int OUT>
+__global__ void __launch_bounds__(192, 1) product_narrow_kernel(const __grid_constant__ CUtensorMap w_map,
+                                                                const __grid_constant__ CUtensorMap x_map,
+                                                                const __grid_constant__ ProductArgs a) {
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ __align__(8) uint64_t bars[2 * 16 + 1];
+    __shared__ uint32_t tmem_base;
+    __shared__ int failed;
+    const uint32_t base = (smem_u32(smem_raw) + 1023) & ~1023u;
+    const int tid = threadIdx.x, warp = tid / 32;
+    const int split = gridDim.x, part = blockIdx.x, tile = blockIdx.y;
+    const int c0 = static_cast<int>(static_cast<int64_t>(a.chunks) * part / split);
+    const int c1 = static_cast<int>(static_cast<int64_t>(a.chunks) * (part + 1) / split);
+    const uint32_t full = smem_u32(bars), empty = full + 8 * a.stages, done = full + 16 * a.stages;
+    const uint32_t b_bytes = a.bn * kChunkBytes, stage_bytes = kABytes + b_bytes;
+    if (tid == 0) {
+        for (int s = 0; s < a.stages; s++) {
+            bar_init(full + 8 * s, 1);
+            bar_init(empty + 8 * s, 1);
+        }
+        bar_init(done, 1);
+        fence_bar_init();
+        failed = 0;
+        prefetch_map(&w_map);
+        prefetch_map(&x_map);
+    }
+    if (warp == 0) tmem_alloc<1>(smem_u32(&tmem_base), a.tmem_cols);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_base;
+    wait_for_prior_grid();
+    bool ok = true;
+    if (warp == 4) {
+        if (elect_one()) {
+            for (int c = c0; c < c1; c++) {
+                const int i = c - c0, s = i % a.stages, round = i / a.stages;
+                if (round > 0 && !bar_wait(empty + 8 * s, (round - 1) & 1)) {
+                    ok = false;
+                    break;
+                }
+                bar_expect(full + 8 * s, stage_bytes + a.tx_extra);
+                tma_2d(base + s * stage_bytes, &w_map, full + 8 * s, c * kChunkBytes, tile * kTileRows);
+                tma_2d(base + s * stage_bytes + kABytes, &x_map, full + 8 * s, c * kChunkBytes, 0);
+            }
+        }
+    } else if (warp == 5) {
+        if (elect_one()) {
+            for (int c = c0; c < c1; c++) {
+                const int i = c - c0, s = i % a.stages, round = i / a.stages;
+                if (!bar_wait(full + 8 * s, round & 1)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint64_t da = operand_desc(base + s * stage_bytes, 16, 1024);
+                const uint64_t db = operand_desc(base + s * stage_bytes + kABytes, 16, 1024);
+#pragma unroll
+                for (int k = 0; k < kChunkBytes / 32; k++) mma_i8<1>(tmem, da + 2 * k, db + 2 * k, a.idesc, i > 0 || k > 0);
+                mma_commit(empty + 8 * s);
+            }
+            if (ok) mma_commit(done);
+        }
+    } else {
+        ok = bar_wait(done, 0);
+        tc_fence_after();
+    }
+    if (!ok) failed = 1;
+    __syncwarp();
+    __syncthreads();
+    const bool bad = failed != 0;
+    if (bad) {
+        if (tid == 0) set_status(a.status, ENTRO_E_TIMEOUT);
+        drain();
+    }
+    const int per = (a.bn + split - 1) / split;  // tokens that a CTA of the cluster finishes
+    const int n = tile * kTileRows + tid;        // (warps 0 to 3)
+    Channel ch;
+    if (warp < 4) ch.load(a, n);
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+    const bool in64 = __any_sync(~0u, warp < 4 && ch.wide) || a.cols > 32768;
+    if (split == 1) {
+        if (warp < 4 && !bad) {
+            for (int t0 = 0; t0 < a.bn; t0 += 16) {
+                uint32_t r[16];
+                tmem_ld16(lanes + t0, r);
+                tmem_wait_ld<16>(r);
+#pragma unroll
+                for (int j = 0; j < 16; j++) {
+                    const int t = t0 + j;
+                    if (t < a.tokens && n < a.rows)
+                        store_out(a.y, t * a.ldy + n, ch.value(static_cast<int32_t>(r[j]), a.x_sum[t], a.x_scale[t], in64), OUT);
+                }
+            }
+        }
+    } else {
+        // [source CTA][token of the share][row]: every CTA's operands have been consumed behind the barrier
+        cluster_sync();
+        if (warp < 4) {
+            for (int t0 = 0; t0 < a.bn; t0 += 16) {
+                uint32_t r[16];
+                tmem_ld16(lanes + t0, r);
+                tmem_wait_ld<16>(r);
+#pragma unroll
+                for (int j = 0; j < 16; j++) {
+                    const int t = t0 + j, owner = t / per;
+                    const uint32_t to = map_to(base + ((part * per + t - owner * per) * kTileRows + tid) * 4, owner);
+                    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(to), "r"(r[j]) : "memory");
+                }
+            }
+        }
+        cluster_sync();
+        if (warp < 4 && !bad) {
+            for (int j = 0; j < per; j++) {
+                const int t = part * per + j;
+                if (t >= a.tokens || t >= a.bn) break;
+                int32_t acc = 0;
+                for (int s = 0; s < split; s++) {
+                    int32_t v;
+                    asm volatile("ld.shared.s32 %0, [%1];" : "=r"(v) : "r"(base + ((s * per + j) * kTileRows + tid) * 4));
+                    acc += v;
+                }
+                if (n < a.rows) store_out(a.y, t * a.ldy + n, ch.value(acc, a.x_sum[t], a.x_scale[t], in64), OUT);
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 0) tmem_free<1>(tmem, a.tmem_cols);
+}
+
+// Many tokens: pairs of CTAs walk the tiles of 256 weight rows by bn tokens.
+// Each CTA brings its 128 rows and half of the tokens, the pair's MMAs (issued
+// by CTA 0) read both halves from both SMs, so a tile of 256 x 256 costs each SM
+// 32 KB of copies per 128 of k.  Two accumulators in TMEM: a tile's epilogue
+// runs beside the next tile's MMAs.
+template <int OUT>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1)
+    product_wide_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__ CUtensorMap x_map,
+                        const __grid_constant__ ProductArgs a) {
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ __align__(8) uint64_t bars[2 * 8 + 4];
+    __shared__ uint32_t tmem_base;
+    __shared__ int failed, epilogue_failed;
+    __shared__ float xs[2][256];
+    __shared__ int32_t xz[2][256];
+    const uint32_t base = (smem_u32(smem_raw) + 1023) & ~1023u;
+    const int tid = threadIdx.x, warp = tid / 32;
+    const uint32_t rank = cluster_rank();
+    const uint32_t full = smem_u32(bars), empty = full + 8 * a.stages, acc_full = full + 16 * a.stages, acc_empty = acc_full + 16;
+    const int half = a.bn / 2;
+    const uint32_t b_bytes = half * kChunkBytes, stage_bytes = kABytes + b_bytes;
+    if (tid == 0) {
+        for (int s = 0; s < a.stages; s++) {
+            bar_init(full + 8 * s, 1);
+            bar_init(empty + 8 * s, 1);
+        }
+        for (int s = 0; s < 2; s++) {
+            bar_init(acc_full + 8 * s, 1);
+            bar_init(acc_empty + 8 * s, 8);  // four epilogue warps of both CTAs
+        }
+        fence_bar_init();
+        failed = epilogue_failed = 0;
+        prefetch_map(&w_map);
+        prefetch_map(&x_map);
+    }
+    if (warp == 2) tmem_alloc<2>(smem_u32(&tmem_base), 512);
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem = tmem_base;
+    wait_for_prior_grid();
+    const int tiles = a.row_tiles * a.token_tiles, pairs = gridDim.x / 2;
+    // groups of 8 row tiles, rows fastest: the tiles in flight share weights and tokens in L2
+    auto where = [&](int i, int &row, int &token) {
+        const int per_group = 8 * a.token_tiles, g = i / per_group, r = i - g * per_group;
+        const int high = min(8, a.row_tiles - g * 8);
+        row = g * 8 + r % high;
+        token = r / high;
+    };
+    bool ok = true;
+    if (warp == 0) {
+        if (elect_one()) {
+            int i = 0;
+            for (int tile = blockIdx.x / 2; tile < tiles && ok; tile += pairs) {
+                int row, token;
+                where(tile, row, token);
+                for (int c = 0; c < a.chunks; c++, i++) {
+                    const int s = i % a.stages, round = i / a.stages;
+                    if (round > 0 && !bar_wait(empty + 8 * s, (round - 1) & 1)) {
+                        ok = false;
+                        break;
+                    }
+                    if (rank == 0) bar_expect(full + 8 * s, 2 * stage_bytes + a.tx_extra);
+                    const uint32_t bar = map_to(full + 8 * s, 0);
+                    tma_2d_pair(base + s * stage_bytes, &w_map, bar, c * kChunkBytes, row * 256 + rank * kTileRows);
+                    tma_2d_pair(base + s * stage_bytes + kABytes, &x_map, bar, c * kChunkBytes, token * a.bn + rank * half);
+                }
+            }
+        }
+    } else if (warp == 1 && rank == 0) {
+        if (elect_one()) {
+            int i = 0, n = 0;
+            for (int tile = blockIdx.x / 2; tile < tiles && ok; tile += pairs, n++) {
+                const int acc = n & 1;
+                if (n >= 2 && !bar_wait(acc_empty + 8 * acc, (n / 2 - 1) & 1)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                for (int c = 0; c < a.chunks; c++, i++) {
+                    const int s = i % a.stages, round = i / a.stages;
+                    if (!bar_wait(full + 8 * s, round & 1)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint64_t da = operand_desc(base + s * stage_bytes, 16, 1024);
+                    const uint64_t db = operand_desc(base + s * stage_bytes + kABytes, 16, 1024);
+#pragma unroll
+                    for (int k = 0; k < kChunkBytes / 32; k++)
+                        mma_i8<2>(tmem + acc * 256, da + 2 * k, db + 2 * k, a.idesc, c > 0 || k > 0);
+                    mma_commit_pair(empty + 8 * s);
+                }
+                if (ok) mma_commit_pair(acc_full + 8 * acc);
+            }
+        }
+    } else if (warp >= 4) {
+        const int e = warp - 4, et = tid - 128;
+        int n = 0;
+        for (int tile = blockIdx.x / 2; tile < tiles; tile += pairs, n++) {
+            const int acc = n & 1;
+            int row, token;
+            where(tile, row, token);
+            // the tile's token scales and sums, read while its MMAs run; every epilogue warp has
+            // left this buffer's previous tile when the one after that tile's barrier below is passed
+            for (int j = et; j < a.bn; j += 128) {
+                const int t = token * a.bn + j;
+                xs[acc][j] = t < a.tokens ? a.x_scale[t] : 0.0f;
+                xz[acc][j] = t < a.tokens ? a.x_sum[t] : 0;
+            }
+            asm volatile("bar.sync 1, 128;" ::: "memory");
+            const int ch_row = row * 256 + rank * kTileRows + et;
+            Channel ch;
+            ch.load(a, ch_row);
+            const bool in64 = __any_sync(~0u, ch.wide) || a.cols > 32768;
+            ok = bar_wait(acc_full + 8 * acc, (n / 2) & 1);
+            if (!ok) epilogue_failed = 1;
+            asm volatile("bar.sync 1, 128;" ::: "memory");  // all four warps stop at the same tile
+            if (*static_cast<volatile int *>(&epilogue_failed)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            const uint32_t lanes = tmem + acc * 256 + (static_cast<uint32_t>(e * 32) << 16);
+            for (int t0 = 0; t0 < a.bn; t0 += 32) {
+                uint32_t r[32];
+                tmem_ld32(lanes + t0, r);
+                tmem_wait_ld<32>(r);
+                const int t = token * a.bn + t0;
+                if (ch_row < a.rows) {
+#pragma unroll
+                    for (int j = 0; j < 32; j++)
+                        if (t + j < a.tokens)
+                            store_out(a.y, (t + j) * a.ldy + ch_row,
+                                      ch.value(static_cast<int32_t>(r[j]), xz[acc][t0 + j], xs[acc][t0 + j], in64), OUT);
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (tid % 32 == 0) bar_arrive_cluster(map_to(acc_empty + 8 * acc, 0));
+        }
+    }
+    if (!ok) failed = 1;
+    __syncwarp();
+    __syncthreads();
+    if (failed) {
+        if (tid == 0) set_status(a.status, ENTRO_E_TIMEOUT);
+        drain();
+    }
+    tc_fence_before();
+    cluster_sync();
+    tc_fence_after();
+    if (warp == 2) tmem_free<2>(tmem, 512);
+}
+
+// ------------------------------------------------------------------ host side
+
+template <typename T>
+static const void *pick_quantize(int vecs) {
+    switch (vecs) {
+        case 1: return reinterpret_cast<const void *>(quantize_kernel<T, 1>);
+        case 2: return reinterpret_cast<const void *>(quantize_kernel<T, 2>);
+        case 4: return reinterpret_cast<const void *>(quantize_kernel<T, 4>);
+        case 8: return reinterpret_cast<const void *>(quantize_kernel<T, 8>);
+        default: return reinterpret_cast<const void *>(quantize_kernel<T, 0>);
+    }
+}
+
+}  // namespace entro
+
+using namespace entro;
+
+extern "C" int entro_quantize_tokens(const void *d_x, int32_t type, int64_t tokens, int64_t cols, int64_t ldx, int8_t *d_q,
+                                     int64_t ldq, float *d_scale, int32_t *d_sum, void *stream) {
+    if ((type != ENTRO_BF16 && type != ENTRO_F16) || tokens < 0 || cols < 1 || ldx < cols || ldq < cols) return ENTRO_E_INVAL;
+    if (tokens > ENTRO_PRODUCT_MAX_TOKENS || cols > ENTRO_PRODUCT_MAX_COLS) return ENTRO_E_LIMIT;
+    if (tokens == 0) return ENTRO_OK;
+    if (!d_x || !d_q || !d_scale || !d_sum || ldq % 16 || !aligned16(d_q) || (reinterpret_cast<uintptr_t>(d_x) & 1)) return ENTRO_E_INVAL;
+    int vecs = 0;
+    if (aligned16(d_x) && ldx % 8 == 0) {
+        const int64_t need = (cols + kQuantThreads * 8 - 1) / (kQuantThreads * 8);
+        vecs = need <= 1 ? 1 : need <= 2 ? 2 : need <= 4 ? 4 : need <= 8 ? 8 : 0;
+    }
+    QuantArgs a{static_cast<const uint16_t *>(d_x), d_q, d_scale, d_sum, tokens, cols, ldx, ldq};
+    const void *fn = type == ENTRO_BF16 ? pick_quantize<__nv_bfloat16>(vecs) : pick_quantize<__half>(vecs);
+    void *args[] = {&a};
+    cudaError_t e = launch_ex(fn, dim3(static_cast<unsigned>(tokens)), kQuantThreads, 0, static_cast<cudaStream_t>(stream), 1, false, args);
+    return e == cudaSuccess ? ENTRO_OK : cuda_fail(e, "entro_quantize_tokens");
+}
+
+extern "C" int entro_unpack_codes(const void *d_codes, int32_t bits, int64_t rows, int64_t cols, void *d_out, int64_t ld, void *stream) {
+    if ((bits != 4 && bits != 8) || rows < 0 || cols < 0 || ld < cols || ld % 16) return ENTRO_E_INVAL;
+    if (rows == 0 || cols == 0) return ENTRO_OK;
+    if (!d_codes || !d_out || !aligned16(d_codes) || !aligned16(d_out) || d_codes == d_out) return ENTRO_E_INVAL;
+    const int64_t words = rows * (ld / 16);
+    const uint8_t *codes = static_cast<const uint8_t *>(d_codes);
+    uint8_t *out = static_cast<uint8_t *>(d_out);
+    void *args[] = {&codes, &bits, &rows, &cols, &out, &ld};
+    cudaError_t e = launch_ex(reinterpret_cast<const void *>(unpack_kernel), dim3(static_cast<unsigned>(std::min<int64_t>((words + 255) / 256, 148 * 16))),
+                              256, 0, static_cast<cudaStream_t>(stream), 1, false, args);
+    return e == cudaSuccess ? ENTRO_OK : cuda_fail(e, "entro_unpack_codes");
+}
+
+extern "C" int entro_matmul_i8(const int8_t *d_q, int64_t ldq, const float *d_x_scale, const int32_t *d_x_sum, int64_t tokens,
+                               const void *d_w, int32_t w_type, int64_t ldw, int64_t rows, int64_t cols, const float *d_w_scale,
+                               float w_scale, const int32_t *d_w_zero, int32_t w_zero, void *d_y, int32_t y_type, int64_t ldy,
+                               int32_t *d_status, void *stream) {
+    if (tokens < 0 || rows < 0 || cols < 1 || ldq < cols || ldw < cols || ldy < rows) return ENTRO_E_INVAL;
+    if ((w_type != ENTRO_U8 && w_type != ENTRO_S8) || (y_type != ENTRO_F32 && y_type != ENTRO_BF16 && y_type != ENTRO_F16)) return ENTRO_E_INVAL;
+    if (tokens > ENTRO_PRODUCT_MAX_TOKENS || cols > ENTRO_PRODUCT_MAX_COLS || rows > (INT64_C(1) << 30)) return ENTRO_E_LIMIT;
+    if (tokens == 0 || rows == 0) return ENTRO_OK;
+    if (!d_q || !d_x_scale || !d_x_sum || !d_w || !d_y) return ENTRO_E_INVAL;
+    if (ldq % 16 || ldw % 16 || !aligned16(d_q) || !aligned16(d_w)) return ENTRO_E_INVAL;
+    if (reinterpret_cast<uintptr_t>(d_y) & (y_type == ENTRO_F32 ? 3 : 1)) return ENTRO_E_INVAL;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+    DeviceInfo di;
+    int r = device_info(dev, &di);
+    if (r != ENTRO_OK) return r;
+
+    ProductArgs a;
+    std::memset(&a, 0, sizeof(a));
+    a.x_scale = d_x_scale;
+    a.x_sum = d_x_sum;
+    a.w_scale = d_w_scale;
+    a.w_zero = d_w_zero;
+    a.w_scale_all = w_scale;
+    a.w_zero_all = w_zero;
+    a.y = d_y;
+    a.ldy = ldy;
+    a.status = d_status;
+    a.tokens = static_cast<int>(tokens);
+    a.rows = static_cast<int>(rows);
+    a.cols = static_cast<int>(cols);
+    a.chunks = static_cast<int>((cols + kChunkBytes - 1) / kChunkBytes);
+    a.tx_extra = test_tx_extra();
+    const uint32_t types = kAccS32 | (w_type == ENTRO_S8 ? kAS8 : kAU8) | kBS8;
+    const bool narrow = tokens <= 256;
+    size_t smem;
+    dim3 grid;
+    unsigned cluster, threads;
+    const void *fn;
+    if (narrow) {
+        a.bn = static_cast<int>((tokens + 15) / 16 * 16);
+        a.row_tiles = static_cast<int>((rows + kTileRows - 1) / kTileRows);
+        int split = 1;
+        while (split < 8 && split * 2 <= a.chunks && a.row_tiles * split * 2 <= di.sms) split *= 2;
+        const int stage = kABytes + a.bn * kChunkBytes;
+        a.stages = std::min(8, 100 * 1024 / stage < 3 ? 200 * 1024 / stage : 100 * 1024 / stage);
+        a.tmem_cols = 32;
+        while (a.tmem_cols < static_cast<uint32_t>(a.bn)) a.tmem_cols *= 2;
+        a.idesc = types | mma_shape(kTileRows, a.bn);
+        const int share = (a.bn + split - 1) / split;
+        smem = 1024 + std::max<size_t>(static_cast<size_t>(a.stages) * stage, static_cast<size_t>(split) * share * kTileRows * 4);
+        grid = dim3(split, a.row_tiles);
+        cluster = split;
+        threads = 192;
+        fn = y_type == ENTRO_F32 ? reinterpret_cast<const void *>(product_narrow_kernel<OUT_F32>)
+             : y_type == ENTRO_BF16 ? reinterpret_cast<const void *>(product_narrow_kernel<OUT_BF16T>)
+                                    : reinterpret_cast<const void *>(product_narrow_kernel<OUT_F16T>);
+        if (a.row_tiles > 65535) return ENTRO_E_LIMIT;
+    } else {
+        // the tile width whose waves cost least (a wave of the pairs takes about bn, and a fixed part)
+        const int pairs = di.sms / 2;
+        a.row_tiles = static_cast<int>((rows + 255) / 256);
+        int64_t best = INT64_MAX;
+        for (int bn = 256; bn >= 128; bn -= 32) {
+            const int64_t tiles = (tokens + bn - 1) / bn * a.row_tiles, cost = (tiles + pairs - 1) / pairs * (bn + 16);
+            if (cost < best) best = cost, a.bn = bn;
+        }
+        a.token_tiles = static_cast<int>((tokens + a.bn - 1) / a.bn);
+        const int stage = kABytes + a.bn / 2 * kChunkBytes;
+        a.stages = std::min(8, 200 * 1024 / stage);
+        a.idesc = types | mma_shape(256, a.bn);
+        smem = 1024 + static_cast<size_t>(a.stages) * stage;
+        const int64_t tiles = static_cast<int64_t>(a.row_tiles) * a.token_tiles;
+        if (tiles > INT32_MAX) return ENTRO_E_LIMIT;
+        grid = dim3(2 * static_cast<unsigned>(std::min<int64_t>(tiles, pairs)));
+        cluster = 1;  // the pair is the kernel's own cluster size
+        threads = 256;
+        fn = y_type == ENTRO_F32 ? reinterpret_cast<const void *>(product_wide_kernel<OUT_F32>)
+             : y_type == ENTRO_BF16 ? reinterpret_cast<const void *>(product_wide_kernel<OUT_BF16T>)
+                                    : reinterpret_cast<const void *>(product_wide_kernel<OUT_F16T>);
+    }
+    r = allow_smem(fn, dev);
+    if (r != ENTRO_OK) return r;
+    CUtensorMap w_map, x_map;
+    const uint64_t w_dims[2] = {static_cast<uint64_t>(cols), static_cast<uint64_t>(rows)}, w_strides[1] = {static_cast<uint64_t>(ldw)};
+    const uint64_t x_dims[2] = {static_cast<uint64_t>(cols), static_cast<uint64_t>(tokens)}, x_strides[1] = {static_cast<uint64_t>(ldq)};
+    const uint32_t w_box[2] = {kChunkBytes, kTileRows}, x_box[2] = {kChunkBytes, static_cast<uint32_t>(narrow ? a.bn : a.bn / 2)};
+    r = encode_map(&w_map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, d_w, w_dims, w_strides, w_box);
+    if (r == ENTRO_OK) r = encode_map(&x_map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, d_q, x_dims, x_strides, x_box);
+    if (r != ENTRO_OK) return r;
+    void *args[] = {&w_map, &x_map, &a};
+    const bool early = static_cast<int64_t>(grid.x) * grid.y <= di.sms;
+    e = launch_ex(fn, grid, threads, smem, static_cast<cudaStream_t>(stream), cluster, early, args);
+    return e == cudaSuccess ? ENTRO_OK : cuda_fail(e, "entro_matmul_i8");
+}

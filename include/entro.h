@@ -218,6 +218,60 @@ ENTRO_API int entro_decode_gemv_group_static(const entro_tensor *const *tensors,
                                              float *const *ys, int32_t count, int32_t batch, int32_t *d_status,
                                              void *stream);
 
+/* ------------------------------------------------------------------------
+ * Around the coded weights: what a model that is served from them computes
+ * besides single tokens' products -- products of a whole prompt, attention
+ * over the prompt, and attention over an 8-bit key/value cache.  Not on the
+ * EntroLLM or LazyWeights pages.  The calls below run on the current device,
+ * which must be the one that holds their buffers.  Their kernels are launched
+ * so that they may start while the kernel before them on the stream finishes;
+ * they touch memory only after it has completed.  Nothing is allocated, on the
+ * host heap or on the device, and all calls may be captured into graphs.
+ * ------------------------------------------------------------------------ */
+
+/* Element types. */
+#define ENTRO_F32 0
+#define ENTRO_BF16 1
+#define ENTRO_F16 2
+#define ENTRO_U8 3
+#define ENTRO_S8 4
+
+#define ENTRO_PRODUCT_MAX_COLS 65536      /* sums of 127 * 255 * cols stay in 32 bits */
+#define ENTRO_PRODUCT_MAX_TOKENS 16777216
+
+/* Activations to 8 bits, with a scale for each token.  For row t of x
+ * (type ENTRO_BF16 or ENTRO_F16, [tokens, cols], rows ldx elements apart):
+ * a = max_k |x[t,k]|, d_scale[t] = a / 127 (fp32), d_q[t*ldq + k] =
+ * 127 x[t,k] / a to the nearest whole number (ties to even, exactly), d_sum[t] =
+ * sum_k d_q[t,k].  A row of zeros gets scale 0; a row that holds an infinity or
+ * NaN gets scale NaN and codes 0.  d_q must be 16-byte aligned and ldq a
+ * multiple of 16; bytes between cols and ldq are left or set to 0. */
+ENTRO_API int entro_quantize_tokens(const void *d_x, int32_t type, int64_t tokens, int64_t cols, int64_t ldx, int8_t *d_q,
+                                    int64_t ldq, float *d_scale, int32_t *d_sum, void *stream);
+
+/* Packed codes (what entro_decode_codes writes: bits 4 or 8, [rows, cols]
+ * without padding) to one byte each in rows of ld bytes: the weights of
+ * entro_matmul_i8 for 4-bit tensors and for cols that are no multiple of 16.
+ * d_codes and d_out 16-byte aligned and apart, ld a multiple of 16. */
+ENTRO_API int entro_unpack_codes(const void *d_codes, int32_t bits, int64_t rows, int64_t cols, void *d_out, int64_t ld,
+                                 void *stream);
+
+/* The product of quantized activations and 8-bit weights: for t < tokens and
+ * n < rows,
+ *   y[t*ldy + n] = x_scale[t] * ws[n] * (sum_k q[t,k] w[n,k] - wz[n] * sum_k q[t,k])
+ * with the sums exact in integers and one fp32 product of the scales.  q, x_scale
+ * and x_sum as entro_quantize_tokens writes them; w [rows, cols] of type
+ * ENTRO_U8 or ENTRO_S8, rows ldw bytes apart; ws from d_w_scale (fp32 [rows]) or,
+ * if that is NULL, w_scale for all; wz from d_w_zero (int32 [rows]) or w_zero (a
+ * tensor's scale and zero point: entro_info).  y_type ENTRO_F32, ENTRO_BF16 or
+ * ENTRO_F16 (rounded to nearest even).  d_q and d_w 16-byte aligned, ldq and ldw
+ * multiples of 16; cols of any size up to ENTRO_PRODUCT_MAX_COLS.  tokens or rows
+ * may be 0.  Results do not depend on how a call is split or batched. */
+ENTRO_API int entro_matmul_i8(const int8_t *d_q, int64_t ldq, const float *d_x_scale, const int32_t *d_x_sum, int64_t tokens,
+                              const void *d_w, int32_t w_type, int64_t ldw, int64_t rows, int64_t cols,
+                              const float *d_w_scale, float w_scale, const int32_t *d_w_zero, int32_t w_zero, void *d_y,
+                              int32_t y_type, int64_t ldy, int32_t *d_status, void *stream);
+
 /* Launch overlap (not in the pages: a B200 launch option).  When enabled,
  * decode launches that fill each SM with one or two large CTAs (the lanes-
  * format kernels on tensors large enough for it) are made with programmatic
