@@ -47,6 +47,13 @@ class _Opts(ctypes.Structure):
                 ("lanes", ctypes.c_int32)]
 
 
+class _KVCache(ctypes.Structure):
+    _fields_ = [("k_codes", ctypes.c_void_p), ("v_codes", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("k_tail", ctypes.c_void_p), ("v_tail", ctypes.c_void_p),
+                ("pages", ctypes.c_int64), ("slots", ctypes.c_int64), ("kv_heads", ctypes.c_int32),
+                ("page_tokens", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("type", ctypes.c_int32)]
+
+
 class _Info(ctypes.Structure):
     _fields_ = [("bits", ctypes.c_int32), ("scheme", ctypes.c_int32), ("max_len", ctypes.c_int32),
                 ("format", ctypes.c_int32), ("rows", ctypes.c_int64), ("cols", ctypes.c_int64),
@@ -62,7 +69,8 @@ EXPORTS = ["entro_encode", "entro_blob_from_bytes", "entro_blob_bytes", "entro_b
            "entro_decode_dequant_bf16", "entro_decode_gemv", "entro_group_table_bytes", "entro_group_prepare",
            "entro_group_launch", "entro_group_free", "entro_strerror", "entro_version", "entro_last_cuda_error",
            "entro_decode_gemv_group_static", "entro_set_overlap", "entro_test_stall_tables",
-           "entro_quantize_tokens", "entro_unpack_codes", "entro_matmul_i8"]
+           "entro_quantize_tokens", "entro_unpack_codes", "entro_matmul_i8",
+           "entro_kv_append", "entro_kv_read", "entro_kv_attend_workspace", "entro_kv_attend"]
 
 
 def _load() -> ctypes.CDLL:
@@ -95,6 +103,10 @@ def _load() -> ctypes.CDLL:
         "entro_decode_gemv_group_static": ([P, P, P, I32, I32, P, P], I32),
         "entro_set_overlap": ([I32], I32),
         "entro_test_stall_tables": ([ctypes.c_uint32], ctypes.c_uint32),
+        "entro_kv_append": ([P, P, I64, I64, P, I64, I64, I64, P, P, I64, I32, P, P, I32, P, P], I32),
+        "entro_kv_read": ([P, P, I64, I64, P, I64, I64, I64, P, P, I64, I32, P, I32, P, P], I32),
+        "entro_kv_attend_workspace": ([P, ctypes.POINTER(U64)], I32),
+        "entro_kv_attend": ([P, P, I64, I64, I32, P, I64, I32, P, P, I32, F32, P, I64, I64, P, U64, P, P], I32),
         "entro_quantize_tokens": ([P, I32, I64, I64, I64, P, I64, P, P, P], I32),
         "entro_unpack_codes": ([P, I32, I64, I64, P, I64, P], I32),
         "entro_matmul_i8": ([P, I64, P, P, I64, P, I32, I64, I64, I64, P, F32, P, I32, P, I32, I64, P, P], I32),
@@ -466,6 +478,157 @@ def matmul_i8(x: QuantTokens, w: torch.Tensor, w_scale: Union[float, torch.Tenso
     return out
 
 
+def _rows(t: torch.Tensor, name: str, dtype: torch.dtype, heads: int, dim: int) -> torch.Tensor:
+    """A [tokens, heads, dim] tensor that the kernels can read in 16-byte pieces."""
+    if t.dtype != dtype or t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
+        raise ValueError(f"{name} must be a {dtype} [tokens, {heads}, {dim}] tensor")
+    s = t.stride()
+    if s[2] != 1 or (t.shape[0] > 1 and s[0] % 8) or (heads > 1 and s[1] % 8) or t.data_ptr() % 16:
+        raise ValueError(f"{name} must have adjacent channels, strides that are multiples of 8 and begin on 16 bytes")
+    return t
+
+
+def _strides(t: torch.Tensor):
+    """Token and head stride; those of a single token or head say nothing."""
+    s = t.stride()
+    return (s[0] if t.shape[0] > 1 else 0), (s[1] if t.shape[1] > 1 else 0)
+
+
+def _index(t: torch.Tensor, name: str, shape: tuple):
+    if t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 {list(shape)} tensor")
+
+
+class KVCache:
+    """Keys and values of one layer in 8 bits, in pages with a scale for each page and head (`entro_kv_cache`).
+
+    Made from the caller's buffers -- codes int8 [pages, kv_heads, page_tokens, head_dim], scales fp32 [pages, kv_heads],
+    tails bf16 or fp16 [slots, kv_heads, page_tokens, head_dim] -- or by `KVCache.empty`.  `page_table` int32
+    [batch, width] names the pages of each sequence's blocks in order, `lens` int32 [batch] its tokens, `slots` int32
+    [batch] its tail slot (None: its place in the batch).  These are read on the GPU: an index out of range is reported in
+    `status` (E_INVAL) and skipped."""
+
+    def __init__(self, k_codes: torch.Tensor, v_codes: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor,
+                 k_tail: torch.Tensor, v_tail: torch.Tensor):
+        if k_codes.dim() != 4 or k_tail.dim() != 4:
+            raise ValueError("codes must be [pages, kv_heads, page_tokens, head_dim], tails [slots, kv_heads, page_tokens, head_dim]")
+        pages, kv, page, dim = k_codes.shape
+        slots, dtype = k_tail.shape[0], k_tail.dtype
+        if page not in (16, 32, 64, 128) or dim not in (64, 96, 128):
+            raise ValueError("page_tokens must be 16, 32, 64 or 128 and head_dim 64, 96 or 128")
+        if dtype not in (torch.bfloat16, torch.float16):
+            raise ValueError("tails must be bf16 or fp16")
+        if pages < 1 or slots < 1 or not 1 <= kv <= 65535:
+            raise ValueError("a cache has a page, a slot and a key head at least")
+        for t, name, want, shape in ((k_codes, "k_codes", torch.int8, (pages, kv, page, dim)), (v_codes, "v_codes", torch.int8, (pages, kv, page, dim)),
+                                     (k_scale, "k_scale", torch.float32, (pages, kv)), (v_scale, "v_scale", torch.float32, (pages, kv)),
+                                     (k_tail, "k_tail", dtype, (slots, kv, page, dim)), (v_tail, "v_tail", dtype, (slots, kv, page, dim))):
+            if t.dtype != want or t.shape != shape or not t.is_contiguous() or t.data_ptr() % 16:
+                raise ValueError(f"{name} must be a contiguous {want} {list(shape)} tensor that begins on 16 bytes")
+        self.device = k_codes.device
+        _inputs(self.device, k_codes=k_codes, v_codes=v_codes, k_scale=k_scale, v_scale=v_scale, k_tail=k_tail, v_tail=v_tail)
+        self.k_codes, self.v_codes, self.k_scale, self.v_scale, self.k_tail, self.v_tail = k_codes, v_codes, k_scale, v_scale, k_tail, v_tail
+        self.pages, self.kv_heads, self.page_tokens, self.head_dim, self.slots, self.dtype = pages, kv, page, dim, slots, dtype
+        self._c = _KVCache(k_codes.data_ptr(), v_codes.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), k_tail.data_ptr(),
+                           v_tail.data_ptr(), pages, slots, kv, page, dim, _TYPES[dtype])
+        self._ref = ctypes.byref(self._c)
+        self._work_bytes = None
+
+    @classmethod
+    def empty(cls, pages: int, kv_heads: int, head_dim: int, page_tokens: int = 64, slots: int = 1,
+              dtype: torch.dtype = torch.bfloat16, device=None) -> "KVCache":
+        device = torch.device("cuda" if device is None else device)
+        codes = [torch.empty((pages, kv_heads, page_tokens, head_dim), dtype=torch.int8, device=device) for _ in range(2)]
+        scales = [torch.empty((pages, kv_heads), dtype=torch.float32, device=device) for _ in range(2)]
+        tails = [torch.empty((slots, kv_heads, page_tokens, head_dim), dtype=dtype, device=device) for _ in range(2)]
+        return cls(*codes, *scales, *tails)
+
+    def _tables(self, page_table: torch.Tensor, slots: Optional[torch.Tensor]) -> int:
+        if page_table.dtype != torch.int32 or page_table.dim() != 2 or (page_table.shape[1] > 1 and page_table.stride(1) != 1):
+            raise ValueError("page_table must be an int32 [batch, width] tensor with adjacent columns")
+        batch = page_table.shape[0]
+        if slots is not None:
+            _index(slots, "slots", (batch,))
+        elif batch > self.slots:
+            raise ValueError("more sequences than tail slots")
+        return batch
+
+    def append(self, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor, page_table: torch.Tensor, lens: torch.Tensor,
+               slots: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
+               stream: Optional[torch.cuda.Stream] = None) -> None:
+        """Packed new tokens k, v [tokens, kv_heads, head_dim] to their sequences; cu_seqlens int32 [batch + 1] says where
+        each sequence's begin, lens counts them already.  No page or slot may be written for two sequences."""
+        _rows(k, "k", self.dtype, self.kv_heads, self.head_dim)
+        _rows(v, "v", self.dtype, self.kv_heads, self.head_dim)
+        if k.shape[0] != v.shape[0]:
+            raise ValueError("k and v must have the same number of tokens")
+        batch = self._tables(page_table, slots)
+        _index(cu_seqlens, "cu_seqlens", (batch + 1,))
+        _index(lens, "lens", (batch,))
+        _inputs(self.device, k=k, v=v, cu_seqlens=cu_seqlens, page_table=page_table, lens=lens, slots=slots, status=status)
+        with _on(self.device, stream) as s:
+            _check(_lib.entro_kv_append(self._ref, k.data_ptr(), *_strides(k), v.data_ptr(), *_strides(v), k.shape[0],
+                                        cu_seqlens.data_ptr(), page_table.data_ptr(), page_table.stride(0) if batch > 1 else page_table.shape[1],
+                                        page_table.shape[1], lens.data_ptr(), slots.data_ptr() if slots is not None else None, batch,
+                                        _dptr(status), s), "entro_kv_append")
+
+    def read(self, page_table: torch.Tensor, cu_seqlens: torch.Tensor, tokens: int, slots: Optional[torch.Tensor] = None,
+             out: Optional[tuple] = None, status: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None):
+        """(k, v) [tokens, kv_heads, head_dim]: all tokens of the sequences, packed; sequence b holds
+        cu_seqlens[b + 1] - cu_seqlens[b] of them."""
+        batch = self._tables(page_table, slots)
+        _index(cu_seqlens, "cu_seqlens", (batch + 1,))
+        if out is not None:
+            for t, name in zip(out, ("k", "v")):
+                _rows(t, name, self.dtype, self.kv_heads, self.head_dim)
+                if t.shape[0] != tokens:
+                    raise ValueError(f"{name} must have {tokens} tokens")
+        _inputs(self.device, cu_seqlens=cu_seqlens, page_table=page_table, slots=slots, status=status,
+                k=out[0] if out is not None else None, v=out[1] if out is not None else None)
+        with _on(self.device, stream) as s:
+            k, v = out if out is not None else (torch.empty((tokens, self.kv_heads, self.head_dim), dtype=self.dtype, device=self.device)
+                                                for _ in range(2))
+            _check(_lib.entro_kv_read(self._ref, k.data_ptr(), *_strides(k), v.data_ptr(), *_strides(v), tokens, cu_seqlens.data_ptr(),
+                                      page_table.data_ptr(), page_table.stride(0) if batch > 1 else page_table.shape[1], page_table.shape[1],
+                                      slots.data_ptr() if slots is not None else None, batch, _dptr(status), s), "entro_kv_read")
+        return k, v
+
+    def attend(self, q: torch.Tensor, page_table: torch.Tensor, lens: torch.Tensor, slots: Optional[torch.Tensor] = None,
+               scale: Optional[float] = None, out: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
+               stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+        """Attention of one token of each sequence, q [batch, heads, head_dim] (heads a multiple of kv_heads), over its
+        cached tokens; scale: 1 / sqrt(head_dim) by default.  A sequence without tokens gets zeros."""
+        heads = q.shape[1] if q.dim() == 3 else 0
+        _rows(q, "q", self.dtype, heads, self.head_dim)
+        if heads < 1 or heads % self.kv_heads:
+            raise ValueError("q's heads must be a multiple of the cache's")
+        batch = self._tables(page_table, slots)
+        if q.shape[0] != batch:
+            raise ValueError("q must have a token for each sequence")
+        _index(lens, "lens", (batch,))
+        if out is not None:
+            _rows(out, "out", self.dtype, heads, self.head_dim)
+            if out.shape[0] != batch:
+                raise ValueError("out must have q's shape")
+        scale = self.head_dim ** -0.5 if scale is None else float(scale)
+        if not 0.0 < scale < 3e38:
+            raise ValueError("scale must be above 0 and finite")
+        _inputs(self.device, q=q, page_table=page_table, lens=lens, slots=slots, out=out, status=status)
+        with _on(self.device, stream) as s:
+            if self._work_bytes is None:
+                n = ctypes.c_uint64()
+                _check(_lib.entro_kv_attend_workspace(self._ref, ctypes.byref(n)), "entro_kv_attend_workspace")
+                self._work_bytes = n.value
+            # a workspace of the call's own, from the pool of the stream it runs on: calls never share one
+            work = torch.empty(self._work_bytes, dtype=torch.uint8, device=self.device)
+            out = torch.empty((batch, heads, self.head_dim), dtype=self.dtype, device=self.device) if out is None else out
+            _check(_lib.entro_kv_attend(self._ref, q.data_ptr(), *_strides(q), heads, page_table.data_ptr(),
+                                        page_table.stride(0) if batch > 1 else page_table.shape[1], page_table.shape[1], lens.data_ptr(),
+                                        slots.data_ptr() if slots is not None else None, batch, scale, out.data_ptr(), *_strides(out),
+                                        work.data_ptr(), self._work_bytes, _dptr(status), s), "entro_kv_attend")
+        return out
+
+
 def test_stall_tables(extra_bytes: int) -> int:
     """Test hook for the bounded waits: later launches wait for `extra_bytes` of table copy that
     never arrive, so each gives up after about a second with E_TIMEOUT in the status word.
@@ -487,7 +650,7 @@ def set_overlap(enable: bool) -> bool:
 
 
 __all__ = ["Blob", "DeviceTensor", "Group", "EntroError", "encode", "upload", "lib", "version", "set_overlap", "EXPORTS",
-           "decode_gemv_group_static", "STATIC_GROUP_MAX", "QuantTokens", "quantize_tokens", "matmul_i8",
+           "decode_gemv_group_static", "STATIC_GROUP_MAX", "QuantTokens", "quantize_tokens", "matmul_i8", "KVCache",
            "test_stall_tables", "QUANT_AUTO", "QUANT_UNSIGNED", "QUANT_ASYM", "FORMAT_SINGLE", "FORMAT_LANES", "FORMAT_ROWS_CO",
            "FORMAT_ROWS", "GROUP_GEMV",
            "GROUP_BF16", "SCHEME_UNSIGNED", "SCHEME_ASYM"]

@@ -1,0 +1,845 @@
+// kvcache.cu -- a paged key/value cache in 8 bits with a scale for each block of
+// tokens and head: its writer, its reader, and the attention of single tokens
+// over it.
+//
+// A page holds P tokens of all key heads, [head][token][channel], and is the
+// block that shares a scale.  A block is coded once it is full: with a the
+// largest magnitude of the block and head, scale = a / 127 and codes =
+// rint(127 x / a).  The tokens of a sequence's last, open block stay in 16 bits
+// in the sequence's tail slot.  So codes are never coded again, and what a cache
+// holds does not depend on how its tokens arrived.
+#include <algorithm>
+#include <cstring>
+
+#include "launch.h"
+#include "sm100.cuh"
+
+namespace entro {
+using namespace sm100;
+
+struct Cache {
+    int8_t *codes[2];  // keys, values: [pages][kv][P][D]
+    float *scale[2];   // [pages][kv]
+    void *tail[2];     // [slots][kv][P][D], 16-bit
+    int64_t pages, slots;
+    int kv, log_page;
+};
+
+// ------------------------------------------------------------------ append
+
+struct AppendArgs {
+    Cache c;
+    const void *in[2];  // [tokens][kv][D]
+    int64_t in_token[2], in_head[2];  // strides, elements
+    const int32_t *cu;     // [batch + 1]: a sequence's new tokens among the packed ones
+    const int32_t *table;  // [batch][table_width]
+    const int32_t *lens;   // [batch]: tokens with the new ones
+    const int32_t *slot_of;
+    int32_t *status;
+    int64_t tokens, table_stride;
+    int batch, table_width;
+};
+
+constexpr int kAppendThreads = 128;
+
+// The sequence's new tokens [begin, begin + n) and its first new position; n = 0
+// for what the arguments do not allow (reported once).
+__device__ __forceinline__ int new_tokens(const AppendArgs &a, int b, int &begin, int &start) {
+    begin = a.cu[b];
+    const int end = a.cu[b + 1], len = a.lens[b], n = end - begin;
+    start = len - n;
+    const int slot = a.slot_of ? a.slot_of[b] : b;
+    if (begin < 0 || n < 0 || end > a.tokens || start < 0 || slot < 0 || slot >= a.c.slots ||
+        (n > 0 && len >> a.c.log_page > a.table_width)) {
+        set_status(a.status, ENTRO_E_INVAL);
+        return 0;
+    }
+    return n;
+}
+
+// Work item -> (sequence, block): an item for each block that gets new tokens.
+__device__ __forceinline__ bool find_block(const AppendArgs &a, int64_t item, int &b, int &block, int &begin, int &n, int &start) {
+    __shared__ int warp_sum[kAppendThreads / 32];
+    __shared__ int found[5];
+    const int tid = threadIdx.x, lane = tid % 32;
+    int64_t before = 0;
+    for (int b0 = 0; b0 < a.batch; b0 += kAppendThreads) {
+        const int mine = b0 + tid;
+        int bg = 0, st = 0, nn = 0, blocks = 0;
+        if (mine < a.batch) {
+            nn = new_tokens(a, mine, bg, st);
+            if (nn > 0) blocks = ((st + nn - 1) >> a.c.log_page) - (st >> a.c.log_page) + 1;
+        }
+        int sum = blocks;
+        for (int o = 1; o < 32; o *= 2) {
+            const int up = __shfl_up_sync(~0u, sum, o);
+            if (lane >= o) sum += up;
+        }
+        if (tid == 0) found[0] = -1;
+        if (lane == 31) warp_sum[tid / 32] = sum;
+        __syncthreads();
+        int64_t at = before + sum;
+        for (int w = 0; w < tid / 32; w++) at += warp_sum[w];
+        if (item < at && item >= at - blocks) {
+            found[0] = mine;
+            found[1] = (st >> a.c.log_page) + static_cast<int>(item - (at - blocks));
+            found[2] = bg;
+            found[3] = nn;
+            found[4] = st;
+        }
+        __syncthreads();
+        if (found[0] >= 0) {
+            b = found[0], block = found[1], begin = found[2], n = found[3], start = found[4];
+            return true;
+        }
+        for (int w = 0; w < kAppendThreads / 32; w++) before += warp_sum[w];
+        __syncthreads();
+    }
+    return false;
+}
+
+// One CTA a (block, head, keys or values).  Bound by memory: 2 bytes of each
+// new element in, 1 (or 2, in the tail) out.
+template <typename T, int D, int P>
+__global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs a) {
+    constexpr int kVecs = P * D / 8, kMine = (kVecs + kAppendThreads - 1) / kAppendThreads, kRow = D / 8;
+    __shared__ uint32_t red[kAppendThreads / 32];
+    int b, block, begin, n, start;
+    if (!find_block(a, blockIdx.x, b, block, begin, n, start)) return;
+    const int tid = threadIdx.x, h = blockIdx.y, kind = blockIdx.z, end = start + n;
+    const int slot = a.slot_of ? a.slot_of[b] : b;
+    const int first = start / P, last_open = end % P ? end / P : -1;  // the block that stays open, if any
+    T *tail = static_cast<T *>(a.c.tail[kind]) + (static_cast<int64_t>(slot) * a.c.kv + h) * (P * D);
+    const T *in = static_cast<const T *>(a.in[kind]) + begin * a.in_token[kind] + h * a.in_head[kind];
+    // When the first block's older tokens are in the tail, its CTA writes the open block's
+    // tokens over them after it has read them; otherwise the open block's own CTA does.
+    const bool older = start % P != 0;
+    if (block != last_open) {
+        const int page = a.table[b * a.table_stride + block];
+        const bool ok = page >= 0 && page < a.c.pages;
+        if (!ok) set_status(a.status, ENTRO_E_INVAL);
+        uint4 v[kMine];
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < kMine; i++) {
+            const int u = i * kAppendThreads + tid;
+            if (kVecs % kAppendThreads && u >= kVecs) break;
+            const int t = u / kRow, x = u % kRow * 8, pos = block * P + t;
+            v[i] = *reinterpret_cast<const uint4 *>(pos < start ? tail + t * D + x : in + (pos - start) * a.in_token[kind] + x);
+            m = __vmaxu2(m, __vmaxu2(__vmaxu2(v[i].x & 0x7FFF7FFFu, v[i].y & 0x7FFF7FFFu),
+                                     __vmaxu2(v[i].z & 0x7FFF7FFFu, v[i].w & 0x7FFF7FFFu)));
+        }
+        m = __reduce_max_sync(~0u, max(m & 0xFFFF, m >> 16));
+        if (tid % 32 == 0) red[tid / 32] = m;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < kAppendThreads / 32; w++) m = max(m, red[w]);
+        const BlockCode<T> code(m);
+        int8_t *out = a.c.codes[kind] + (static_cast<int64_t>(ok ? page : 0) * a.c.kv + h) * (P * D);
+        if (ok) {
+#pragma unroll
+            for (int i = 0; i < kMine; i++) {
+                const int u = i * kAppendThreads + tid;
+                if (kVecs % kAppendThreads && u >= kVecs) break;
+                *reinterpret_cast<uint2 *>(out + u * 8) = code.eight(v[i]);
+            }
+            if (tid == 0) a.c.scale[kind][static_cast<int64_t>(page) * a.c.kv + h] = code.scale();
+        }
+        if (block != first || !older || last_open < 0) return;
+        __syncthreads();  // the older tokens have been read
+    } else if (block != first && older) {
+        return;
+    }
+    // the open block's new tokens into the tail
+    const int from = max(start, last_open * P);
+    for (int u = tid; u < (end - from) * kRow; u += kAppendThreads) {
+        const int pos = from + u / kRow, x = u % kRow * 8;
+        *reinterpret_cast<uint4 *>(tail + pos % P * D + x) =
+            __ldg(reinterpret_cast<const uint4 *>(in + (pos - start) * a.in_token[kind] + x));
+    }
+}
+
+// ------------------------------------------------------------------ read
+
+struct ReadArgs {
+    Cache c;
+    void *out[2];  // [tokens][kv][D]
+    int64_t out_token[2], out_head[2];
+    const int32_t *cu;
+    const int32_t *table;
+    const int32_t *slot_of;
+    int32_t *status;
+    int64_t tokens, table_stride;
+    int batch, table_width;
+};
+
+// Cached tokens back to 16 bits: code times scale in 32 bits, rounded once.  A
+// warp takes a token at a time; bound by memory.
+template <typename T, int D>
+__global__ void __launch_bounds__(256) read_kernel(const ReadArgs a) {
+    const int lane = threadIdx.x % 32, P = 1 << a.c.log_page;
+    const int64_t t = blockIdx.x * 8LL + threadIdx.x / 32;
+    if (t >= a.tokens) return;
+    // the last sequence that begins at or before t
+    int lo = 0, hi = a.batch;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (a.cu[mid] <= t) lo = mid;
+        else hi = mid;
+    }
+    const int b = lo, begin = a.cu[b], end = a.cu[b + 1];
+    if (t < begin || t >= end) return;  // a token of no sequence: left as it is
+    const int pos = static_cast<int>(t) - begin, block = pos >> a.c.log_page;
+    const int slot = a.slot_of ? a.slot_of[b] : b;
+    const bool open = block == (end - begin) >> a.c.log_page;
+    const int page = !open && block < a.table_width ? a.table[b * a.table_stride + block] : -1;
+    if (open ? slot < 0 || slot >= a.c.slots : page < 0 || page >= a.c.pages) {
+        if (lane == 0) set_status(a.status, ENTRO_E_INVAL);
+        return;
+    }
+    constexpr int kRow = D / 8;
+    const int off = pos & (P - 1);
+    for (int u = lane; u < 2 * a.c.kv * kRow; u += 32) {
+        const int x = u % kRow * 8, row = u / kRow, kind = row >= a.c.kv, h = row - kind * a.c.kv;
+        T *out = static_cast<T *>(a.out[kind]) + t * a.out_token[kind] + h * a.out_head[kind] + x;
+        if (open) {
+            const T *tail = static_cast<const T *>(a.c.tail[kind]) + ((static_cast<int64_t>(slot) * a.c.kv + h) * P + off) * D + x;
+            *reinterpret_cast<uint4 *>(out) = __ldg(reinterpret_cast<const uint4 *>(tail));
+            continue;
+        }
+        const int64_t at = static_cast<int64_t>(page) * a.c.kv + h;
+        const float s = __ldg(a.c.scale[kind] + at);
+        const uint2 c = __ldg(reinterpret_cast<const uint2 *>(a.c.codes[kind] + (at * P + off) * D + x));
+        auto two = [&](uint32_t w, int i) {
+            return Half<T>::pack(static_cast<float>(static_cast<int8_t>(w >> (16 * i))) * s,
+                                 static_cast<float>(static_cast<int8_t>(w >> (16 * i + 8))) * s);
+        };
+        *reinterpret_cast<uint4 *>(out) = make_uint4(two(c.x, 0), two(c.x, 1), two(c.y, 0), two(c.y, 1));
+    }
+}
+
+// ------------------------------------------------------------------ attention of single tokens
+
+struct AttendArgs {
+    Cache c;
+    const void *q;  // [batch][heads][D]
+    void *out;      // [batch][heads][D]
+    int64_t q_token, q_head, out_token, out_head, table_stride;
+    const int32_t *table;
+    const int32_t *lens;
+    const int32_t *slot_of;
+    float *work;
+    int32_t *status;
+    int batch, group, chunks;  // query heads of a key head; groups of 8 of them
+    int table_width, ctas;
+    float scale_log2;
+};
+
+constexpr int kAttendThreads = 128;
+constexpr int kTile = 64;         // tokens a CTA takes at a time, 16 a warp
+constexpr int kHeads = 8;         // query heads of an MMA
+constexpr float kLazy = 8.0f;     // the reference maximum is raised when a score passes it by 2^8
+constexpr float kBias = 6.0f;     // weights are held as 2^6 times theirs: at most 2^14 in 16 bits, 2^-30 at least
+
+// The cached length, cut to the table's pages and an open block (both kernels agree on it).
+__device__ __forceinline__ int clean_len(const AttendArgs &a, int b, bool report) {
+    const int len = a.lens[b];
+    const int64_t most = min(((static_cast<int64_t>(a.table_width) + 1) << a.c.log_page) - 1, static_cast<int64_t>(INT32_MAX) - kTile);
+    if (len >= 0 && len <= most) return len;
+    if (report) set_status(a.status, ENTRO_E_INVAL);
+    return len < 0 ? 0 : static_cast<int>(most);
+}
+
+// All (sequence, head, tile)s in a row are cut into equal shares for the CTAs.
+struct Shares {
+    int64_t each, more;  // the first `more` CTAs take one more than `each`
+    __device__ __forceinline__ Shares(int64_t total, int ctas) : each(total / ctas), more(total % ctas) {}
+    __device__ __forceinline__ int64_t begin(int64_t cta) const { return cta * each + min(cta, more); }
+    __device__ __forceinline__ int owner(int64_t tile) const {
+        return static_cast<int>(tile < more * (each + 1) ? tile / (each + 1) : more + (tile - more * (each + 1)) / each);
+    }
+};
+
+// Sums over the batch: all tiles of one head, and those of the sequences before
+// the one that `pick` selects.  pick(tiles before, tiles of this sequence) is
+// true for at most one sequence.
+template <typename Pick>
+__device__ __forceinline__ int64_t scan_batch(const AttendArgs &a, int &seq, int64_t &before, Pick pick) {
+    __shared__ int64_t warp_sum[kAttendThreads / 32], picked_before;
+    __shared__ int picked;
+    const int tid = threadIdx.x, lane = tid % 32;
+    int64_t total = 0;
+    __syncthreads();
+    if (tid == 0) picked = -1;
+    for (int b0 = 0; b0 < a.batch; b0 += kAttendThreads) {
+        const int b = b0 + tid;
+        const int64_t tiles = b < a.batch ? (static_cast<int64_t>(clean_len(a, b, false)) + kTile - 1) / kTile : 0;
+        int64_t sum = tiles;
+        for (int o = 1; o < 32; o *= 2) {
+            const int64_t up = __shfl_up_sync(~0u, sum, o);
+            if (lane >= o) sum += up;
+        }
+        if (lane == 31) warp_sum[tid / 32] = sum;
+        __syncthreads();
+        int64_t at = total + sum - tiles;
+        for (int w = 0; w < kAttendThreads / 32; w++) {
+            if (w < tid / 32) at += warp_sum[w];
+            total += warp_sum[w];
+        }
+        if (b < a.batch && pick(b, at, tiles)) {
+            picked = b;
+            picked_before = at;
+        }
+        __syncthreads();
+    }
+    seq = picked;
+    before = picked_before;
+    return total;
+}
+
+// Four codes to two pairs of 16-bit floats, exactly: 1024 + (code + 128) has the
+// code's byte as its low bits.
+__device__ __forceinline__ uint32_t sub2(uint32_t h) {
+    uint32_t r;
+    asm("sub.f16x2 %0, %1, %2;" : "=r"(r) : "r"(h), "r"(0x64806480u));
+    return r;
+}
+__device__ __forceinline__ void mma16816(float *c, const uint32_t *a, uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// N bytes (8, 12, 16, 24 or 32) from an address aligned to the largest power of two in N
+template <int N>
+__device__ __forceinline__ void load_bytes(uint32_t *r, const void *p) {
+    if (N % 16 == 0) {
+#pragma unroll
+        for (int i = 0; i < N / 16; i++) {
+            const uint4 v = __ldg(static_cast<const uint4 *>(p) + i);
+            r[4 * i] = v.x, r[4 * i + 1] = v.y, r[4 * i + 2] = v.z, r[4 * i + 3] = v.w;
+        }
+    } else if (N % 8 == 0) {
+#pragma unroll
+        for (int i = 0; i < N / 8; i++) {
+            const uint2 v = __ldg(static_cast<const uint2 *>(p) + i);
+            r[2 * i] = v.x, r[2 * i + 1] = v.y;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < N / 4; i++) r[i] = __ldg(static_cast<const uint32_t *>(p) + i);
+    }
+}
+// A power of two that brings numbers of at most this magnitude (the bits of a
+// 16-bit float without its sign) near 2^14, and its inverse: they then fit fp16,
+// and those that lose bits there are below 2^-27 of the largest.
+template <typename T>
+__device__ __forceinline__ float fit_factor(uint32_t top, float &inverse) {
+    if (Half<T>::kExp == 0x7C007C00u) {  // fp16 already
+        inverse = 1.0f;
+        return 1.0f;
+    }
+    const int e = min(max(static_cast<int>(top >> 7), 28), 254);  // biased exponent
+    inverse = __uint_as_float(static_cast<uint32_t>(e - 14) << 23);
+    return __uint_as_float(static_cast<uint32_t>(254 + 14 - e) << 23);
+}
+template <typename T>
+__device__ __forceinline__ uint32_t to_f16x2(uint32_t v, float factor) {
+    if (Half<T>::kExp == 0x7C007C00u) return v;
+    const float2 f = Half<T>::widen(v);
+    return Half<__half>::pack(f.x * factor, f.y * factor);
+}
+
+// A warp's running softmax over the tokens it has seen, for 8 query heads: this
+// thread holds heads 2 tig and 2 tig + 1 (tig = lane % 4) of 1/8 of the channels.
+// Scores and outputs are transposed products, K Q^T and V^T P^T, so that the
+// codes are the 16-row operand: the rows of a thread's fragments are tokens
+// (scores) or channels (outputs), and neither the order of the tokens nor that of
+// the channels inside an MMA matters, so a thread reads whole strips of its rows.
+template <int D>
+struct Running {
+    float m[2], l[2];
+    float o[D / 16][4];
+
+    __device__ __forceinline__ void clear() {
+        m[0] = m[1] = -INFINITY;
+        l[0] = l[1] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < D / 16; i++) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
+    }
+
+    // s: scores in units of log2 (tokens gid and gid + 8 of heads 2 tig, 2 tig + 1), -inf
+    // where there is no token; on return the weights as the P^T operand.
+    __device__ __forceinline__ void weights(const float *s, uint32_t &p0, uint32_t &p1) {
+        const float t0 = m[0] + kLazy, t1 = m[1] + kLazy;
+        if (__any_sync(~0u, s[0] > t0 || s[2] > t0 || s[1] > t1 || s[3] > t1)) {
+            float n0 = fmaxf(s[0], s[2]), n1 = fmaxf(s[1], s[3]);
+#pragma unroll
+            for (int x = 4; x < 32; x *= 2) {
+                n0 = fmaxf(n0, __shfl_xor_sync(~0u, n0, x));
+                n1 = fmaxf(n1, __shfl_xor_sync(~0u, n1, x));
+            }
+            n0 = fmaxf(n0, m[0]), n1 = fmaxf(n1, m[1]);
+            const float f0 = m[0] == n0 ? 1.0f : ex2(m[0] - n0), f1 = m[1] == n1 ? 1.0f : ex2(m[1] - n1);
+            m[0] = n0, m[1] = n1;
+            l[0] *= f0, l[1] *= f1;
+#pragma unroll
+            for (int i = 0; i < D / 16; i++) {
+                o[i][0] *= f0, o[i][2] *= f0;
+                o[i][1] *= f1, o[i][3] *= f1;
+            }
+        }
+        // no score so far: any reference does
+        const float r0 = (m[0] == -INFINITY ? 0.0f : m[0]) - kBias, r1 = (m[1] == -INFINITY ? 0.0f : m[1]) - kBias;
+        const float e0 = ex2(s[0] - r0), e1 = ex2(s[1] - r1), e2 = ex2(s[2] - r0), e3 = ex2(s[3] - r1);
+        l[0] += e0 + e2;
+        l[1] += e1 + e3;
+        p0 = transpose8x8(Half<__half>::pack(e0, e1));
+        p1 = transpose8x8(Half<__half>::pack(e2, e3));
+    }
+};
+
+// One pass over the cache.  A CTA's share of all tiles is one row of tiles, cut
+// where the (sequence, head) changes; a piece that covers all of its sequence and
+// head is finished here, others leave (m, l, o) behind for the join.  Bound by
+// reading the codes (2 D bytes of a token and key head).
+template <typename T, int D>
+__global__ void __launch_bounds__(kAttendThreads, 4) attend_kernel(const AttendArgs a) {
+    constexpr int kK = D / 4, kV = D / 8;  // bytes of a token's codes that a thread reads: keys (2 tokens), values (4)
+    __shared__ float sm_m[4][kHeads], sm_l[4][kHeads];
+    __shared__ __align__(16) float sm_o[4][kHeads][D + 4];  // read and written in pairs
+    wait_for_prior_grid();
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, gid = lane / 4, tig = lane % 4;
+    const int P = 1 << a.c.log_page, cols = a.c.kv * a.chunks;
+    int seq;
+    int64_t before;
+    // first pass for the total, second for the sequence of this share's first tile
+    const int64_t total = scan_batch(a, seq, before, [](int, int64_t, int64_t) { return false; }) * cols;
+    const Shares shares(total, a.ctas);
+    int64_t at = shares.begin(blockIdx.x);
+    const int64_t stop = shares.begin(blockIdx.x + 1);
+    if (at >= stop) return;
+    scan_batch(a, seq, before, [&](int, int64_t b4, int64_t tiles) { return at >= b4 * cols && at < (b4 + tiles) * cols; });
+    int64_t seq_at = before * cols;
+    while (at < stop) {
+        // the piece: tiles [t0, t1) of column (key head, chunk of query heads) of the sequence
+        int len = clean_len(a, seq, true), tiles = (len + kTile - 1) / kTile;
+        while (at >= seq_at + static_cast<int64_t>(tiles) * cols) {  // (sequences without tokens have no tiles)
+            seq_at += static_cast<int64_t>(tiles) * cols;
+            seq++;
+            len = clean_len(a, seq, true);
+            tiles = (len + kTile - 1) / kTile;
+        }
+        const int col = static_cast<int>((at - seq_at) / tiles), t0 = static_cast<int>((at - seq_at) % tiles);
+        const int t1 = static_cast<int>(min(static_cast<int64_t>(tiles), t0 + (stop - at)));
+        const int h = col / a.chunks, head0 = h * a.group + col % a.chunks * kHeads;
+        const int heads = min(kHeads, a.group - col % a.chunks * kHeads);
+        const int full = len >> a.c.log_page << a.c.log_page;  // tokens in coded blocks
+        const int32_t *pages = a.table + seq * a.table_stride;
+
+        // Q as the second operand: head gid, channels tig D / 4 + 4 s + 0 .. 3 in step s
+        uint32_t q[D / 16][2];
+        float mine = 0.0f;
+        {
+            const T *row = static_cast<const T *>(a.q) + seq * a.q_token + (head0 + min(gid, heads - 1)) * a.q_head + tig * kK;
+            uint32_t raw[D / 8], top = 0;
+            load_bytes<D / 2>(raw, row);
+#pragma unroll
+            for (int i = 0; i < D / 8; i++) top = __vmaxu2(top, raw[i] & 0x7FFF7FFFu);
+            top = max(top & 0xFFFF, top >> 16);
+            top = max(top, __shfl_xor_sync(~0u, top, 1));
+            top = max(top, __shfl_xor_sync(~0u, top, 2));
+            const float f = fit_factor<T>(top, mine);
+#pragma unroll
+            for (int i = 0; i < D / 8; i++) q[i / 2][i % 2] = gid < heads ? to_f16x2<T>(raw[i], f) : 0u;
+            mine *= a.scale_log2;
+        }
+        const float qs[2] = {__shfl_sync(~0u, mine, tig * 8), __shfl_sync(~0u, mine, tig * 8 + 4)};
+
+        Running<D> r;
+        r.clear();
+        // 16 tokens a step; a thread's keys are tokens gid and gid + 8, its values tokens 2 tig, 2 tig + 1 and those + 8
+        uint32_t kr[2][kK / 4], vr[4][kV / 4];
+        float ks = 0.0f, vs = 0.0f, next_ks = 0.0f, next_vs = 0.0f;
+        const int8_t *next_k = nullptr, *next_v = nullptr;
+        // where step `tile`'s codes are (null: in the tail, past the end, or on no page)
+        auto locate = [&](int tile) {
+            const int tok = tile * kTile + warp * 16;
+            next_k = next_v = nullptr;
+            if (tile >= t1 || tok >= full) return;
+            const int page = __ldg(pages + (tok >> a.c.log_page));
+            if (page < 0 || page >= a.c.pages) {
+                set_status(a.status, ENTRO_E_INVAL);
+                return;
+            }
+            const int64_t block = static_cast<int64_t>(page) * a.c.kv + h, row = block * P + (tok & (P - 1));
+            next_k = a.c.codes[0] + (row + gid) * D + tig * kK;
+            next_v = a.c.codes[1] + (row + 2 * tig) * D + gid * kV;
+            next_ks = __ldg(a.c.scale[0] + block);
+            next_vs = __ldg(a.c.scale[1] + block);
+        };
+        auto load_k = [&]() {
+            if (next_k) {
+                load_bytes<kK>(kr[0], next_k);
+                load_bytes<kK>(kr[1], next_k + 8 * D);
+            }
+        };
+        auto load_v = [&]() {
+            if (next_v) {
+#pragma unroll
+                for (int j = 0; j < 4; j++) load_bytes<kV>(vr[j], next_v + (j / 2 * 8 + j % 2) * D);
+            }
+        };
+        locate(t0);
+        load_k();
+        load_v();
+        for (int tile = t0; tile < t1; tile++) {
+            const int tok = tile * kTile + warp * 16;
+            const bool coded = next_k != nullptr;
+            ks = next_ks, vs = next_vs;
+            if (coded) {
+                float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int s = 0; s < D / 16; s++) {
+                    const uint32_t lo = kr[0][s] ^ 0x80808080u, hi = kr[1][s] ^ 0x80808080u;
+                    const uint32_t f[4] = {sub2(__byte_perm(lo, 0x64646464u, 0x4140)), sub2(__byte_perm(hi, 0x64646464u, 0x4140)),
+                                           sub2(__byte_perm(lo, 0x64646464u, 0x4342)), sub2(__byte_perm(hi, 0x64646464u, 0x4342))};
+                    mma16816(c, f, q[s][0], q[s][1]);
+                }
+                locate(tile + 1);
+                load_k();  // in flight beside this step's softmax and values
+                const float f0 = qs[0] * ks, f1 = qs[1] * ks;
+                const float s[4] = {c[0] * f0, c[1] * f1, c[2] * f0, c[3] * f1};
+                uint32_t p0, p1;
+                r.weights(s, p0, p1);
+#pragma unroll
+                for (int i = 0; i < D / 32; i++) {
+                    // four channels of four tokens to the fragments of two MMAs
+                    const uint32_t x0 = vr[0][i] ^ 0x80808080u, x1 = vr[1][i] ^ 0x80808080u;
+                    const uint32_t x2 = vr[2][i] ^ 0x80808080u, x3 = vr[3][i] ^ 0x80808080u;
+#pragma unroll
+                    for (int u = 0; u < 2; u++) {
+                        const uint32_t lo = __byte_perm(x0, x1, u ? 0x7362 : 0x5140), hi = __byte_perm(x2, x3, u ? 0x7362 : 0x5140);
+                        const uint32_t f[4] = {sub2(__byte_perm(lo, 0x64646464u, 0x4140)), sub2(__byte_perm(lo, 0x64646464u, 0x4342)),
+                                               sub2(__byte_perm(hi, 0x64646464u, 0x4140)), sub2(__byte_perm(hi, 0x64646464u, 0x4342))};
+                        float w[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                        mma16816(w, f, p0, p1);
+                        float *o = r.o[2 * i + u];
+                        o[0] += w[0] * vs, o[1] += w[1] * vs, o[2] += w[2] * vs, o[3] += w[3] * vs;
+                    }
+                }
+                load_v();
+            } else {
+                const int slot = a.slot_of ? a.slot_of[seq] : seq;
+                const bool slot_ok = slot >= 0 && slot < a.c.slots;
+                if (tok >= full && tok < len && !slot_ok) set_status(a.status, ENTRO_E_INVAL);
+                if (tok >= full && tok < len && slot_ok) {
+                    // up to 16 tokens of the open block, in 16 bits
+                    const int64_t base = (static_cast<int64_t>(slot) * a.c.kv + h) * P + (tok & (P - 1));
+                    const T *kt = static_cast<const T *>(a.c.tail[0]) + base * D, *vt = static_cast<const T *>(a.c.tail[1]) + base * D;
+                    const int n = len - tok;  // tokens of the step that exist, if below 16
+                    float c[4] = {0.0f, 0.0f, 0.0f, 0.0f}, inverse;
+                    {
+                        uint32_t x[2][D / 8], top = 0;
+#pragma unroll
+                        for (int j = 0; j < 2; j++) {
+                            if (gid + 8 * j < n) {
+                                load_bytes<D / 2>(x[j], kt + (gid + 8 * j) * D + tig * kK);
+                            } else {
+#pragma unroll
+                                for (int i = 0; i < D / 8; i++) x[j][i] = 0;
+                            }
+#pragma unroll
+                            for (int i = 0; i < D / 8; i++) top = __vmaxu2(top, x[j][i] & 0x7FFF7FFFu);
+                        }
+                        top = __reduce_max_sync(~0u, max(top & 0xFFFF, top >> 16));
+                        const float f = fit_factor<T>(top, inverse);
+#pragma unroll
+                        for (int s = 0; s < D / 16; s++) {
+                            const uint32_t fr[4] = {to_f16x2<T>(x[0][2 * s], f), to_f16x2<T>(x[1][2 * s], f),
+                                                    to_f16x2<T>(x[0][2 * s + 1], f), to_f16x2<T>(x[1][2 * s + 1], f)};
+                            mma16816(c, fr, q[s][0], q[s][1]);
+                        }
+                    }
+                    const float f0 = qs[0] * inverse, f1 = qs[1] * inverse;
+                    const float s[4] = {gid < n ? c[0] * f0 : -INFINITY, gid < n ? c[1] * f1 : -INFINITY,
+                                        gid + 8 < n ? c[2] * f0 : -INFINITY, gid + 8 < n ? c[3] * f1 : -INFINITY};
+                    uint32_t p0, p1;
+                    r.weights(s, p0, p1);
+                    uint32_t y[4][D / 16], top = 0;
+#pragma unroll
+                    for (int j = 0; j < 4; j++) {
+                        const int t = 2 * tig + j / 2 * 8 + j % 2;
+                        if (t < n) {
+                            load_bytes<D / 4>(y[j], vt + t * D + gid * kV);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < D / 16; i++) y[j][i] = 0;
+                        }
+#pragma unroll
+                        for (int i = 0; i < D / 16; i++) top = __vmaxu2(top, y[j][i] & 0x7FFF7FFFu);
+                    }
+                    top = __reduce_max_sync(~0u, max(top & 0xFFFF, top >> 16));
+                    const float f = fit_factor<T>(top, inverse);
+#pragma unroll
+                    for (int i = 0; i < D / 16; i++) {
+                        uint32_t z[4];
+#pragma unroll
+                        for (int j = 0; j < 4; j++) z[j] = to_f16x2<T>(y[j][i], f);
+                        const uint32_t fr[4] = {__byte_perm(z[0], z[1], 0x5410), __byte_perm(z[0], z[1], 0x7632),
+                                                __byte_perm(z[2], z[3], 0x5410), __byte_perm(z[2], z[3], 0x7632)};
+                        float w[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                        mma16816(w, fr, p0, p1);
+#pragma unroll
+                        for (int j = 0; j < 4; j++) r.o[i][j] += w[j] * inverse;
+                    }
+                }
+                locate(tile + 1);
+                load_k();
+                load_v();
+            }
+        }
+
+        // the four warps' parts meet in shared memory
+#pragma unroll
+        for (int x = 4; x < 32; x *= 2) {
+            r.l[0] += __shfl_xor_sync(~0u, r.l[0], x);
+            r.l[1] += __shfl_xor_sync(~0u, r.l[1], x);
+        }
+        if (gid == 0) {
+            sm_m[warp][2 * tig] = r.m[0], sm_m[warp][2 * tig + 1] = r.m[1];
+            sm_l[warp][2 * tig] = r.l[0], sm_l[warp][2 * tig + 1] = r.l[1];
+        }
+#pragma unroll
+        for (int i = 0; i < D / 16; i++) {
+            // rows gid and gid + 8 of tile i are channels gid D / 8 + 2 i and + 1
+            const int d = gid * kV + 2 * i;
+            *reinterpret_cast<float2 *>(&sm_o[warp][2 * tig][d]) = make_float2(r.o[i][0], r.o[i][2]);
+            *reinterpret_cast<float2 *>(&sm_o[warp][2 * tig + 1][d]) = make_float2(r.o[i][1], r.o[i][3]);
+        }
+        __syncthreads();
+        const bool whole = t0 == 0 && t1 == tiles;
+        // a piece that does not begin its sequence and head goes to the CTA's first place, one that only does not end it to the second
+        float *part = a.work + (static_cast<int64_t>(blockIdx.x) * 2 + (t0 == 0)) * (kHeads * (D + 2));
+        for (int u = tid; u < heads * (D / 2); u += kAttendThreads) {
+            const int head = u / (D / 2), d = u % (D / 2) * 2;
+            float m = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < 4; w++) m = fmaxf(m, sm_m[w][head]);
+            float l = 0.0f, o0 = 0.0f, o1 = 0.0f;
+#pragma unroll
+            for (int w = 0; w < 4; w++) {
+                const float f = sm_m[w][head] == m ? 1.0f : ex2(sm_m[w][head] - m);
+                l += f * sm_l[w][head];
+                o0 += f * sm_o[w][head][d];
+                o1 += f * sm_o[w][head][d + 1];
+            }
+            if (whole) {
+                const float by = l == 0.0f ? 0.0f : 1.0f / l;
+                T *out = static_cast<T *>(a.out) + seq * a.out_token + (head0 + head) * a.out_head + d;
+                *reinterpret_cast<uint32_t *>(out) = Half<T>::pack(o0 * by, o1 * by);
+            } else {
+                float *row = part + head * (D + 2);
+                *reinterpret_cast<float2 *>(row + 2 + d) = make_float2(o0, o1);
+                if (d == 0) *reinterpret_cast<float2 *>(row) = make_float2(m, l);
+            }
+        }
+        __syncthreads();
+        at += t1 - t0;
+    }
+}
+
+// Joins the pieces of each (sequence, key head, chunk): a CTA each.  Sequences
+// without tokens get zeros.
+template <typename T, int D>
+__global__ void __launch_bounds__(kAttendThreads) join_kernel(const AttendArgs a) {
+    wait_for_prior_grid();
+    const int tid = threadIdx.x, cols = a.c.kv * a.chunks;
+    const int seq = static_cast<int>(blockIdx.x / cols), col = static_cast<int>(blockIdx.x % cols);
+    int got;
+    int64_t before;
+    const int64_t total = scan_batch(a, got, before, [&](int b, int64_t, int64_t) { return b == seq; }) * cols;
+    const int h = col / a.chunks, head0 = h * a.group + col % a.chunks * kHeads;
+    const int heads = min(kHeads, a.group - col % a.chunks * kHeads);
+    const int tiles = (clean_len(a, seq, true) + kTile - 1) / kTile;
+    const Shares shares(total, a.ctas);
+    const int64_t t0 = before * cols + static_cast<int64_t>(col) * tiles;
+    int first = 0, last = 0;
+    if (tiles > 0) {
+        first = shares.owner(t0);
+        last = shares.owner(t0 + tiles - 1);
+        if (first == last) return;  // one CTA had it all
+    }
+    for (int u = tid; u < heads * (D / 2); u += kAttendThreads) {
+        const int head = u / (D / 2), d = u % (D / 2) * 2;
+        float m = -INFINITY, l = 0.0f, o0 = 0.0f, o1 = 0.0f;
+        for (int i = first; i <= last && tiles > 0; i++) {
+            const float *row = a.work + ((static_cast<int64_t>(i) * 2 + (i == first)) * kHeads + head) * (D + 2);
+            const float2 ml = *reinterpret_cast<const float2 *>(row), o = *reinterpret_cast<const float2 *>(row + 2 + d);
+            const float n = fmaxf(m, ml.x), fm = m == n ? 1.0f : ex2(m - n), f = ml.x == n ? 1.0f : ex2(ml.x - n);
+            l = l * fm + ml.y * f;
+            o0 = o0 * fm + o.x * f;
+            o1 = o1 * fm + o.y * f;
+            m = n;
+        }
+        const float by = l == 0.0f ? 0.0f : 1.0f / l;
+        T *out = static_cast<T *>(a.out) + seq * a.out_token + (head0 + head) * a.out_head + d;
+        *reinterpret_cast<uint32_t *>(out) = Half<T>::pack(o0 * by, o1 * by);
+    }
+}
+
+// ------------------------------------------------------------------ host side
+
+static int make_cache(const entro_kv_cache *c, Cache *o) {
+    if (!c || c->pages < 1 || c->slots < 1 || c->kv_heads < 1 || c->kv_heads > 65535) return ENTRO_E_INVAL;
+    if (c->type != ENTRO_BF16 && c->type != ENTRO_F16) return ENTRO_E_INVAL;
+    if (c->head_dim != 64 && c->head_dim != 96 && c->head_dim != 128) return ENTRO_E_INVAL;
+    if (c->page_tokens != 16 && c->page_tokens != 32 && c->page_tokens != 64 && c->page_tokens != 128) return ENTRO_E_INVAL;
+    void *const p[6] = {c->k_codes, c->v_codes, c->k_scale, c->v_scale, c->k_tail, c->v_tail};
+    for (void *q : p)
+        if (!q || !aligned16(q)) return ENTRO_E_INVAL;
+    o->codes[0] = static_cast<int8_t *>(c->k_codes), o->codes[1] = static_cast<int8_t *>(c->v_codes);
+    o->scale[0] = static_cast<float *>(c->k_scale), o->scale[1] = static_cast<float *>(c->v_scale);
+    o->tail[0] = c->k_tail, o->tail[1] = c->v_tail;
+    o->pages = c->pages, o->slots = c->slots, o->kv = c->kv_heads;
+    o->log_page = c->page_tokens == 16 ? 4 : c->page_tokens == 32 ? 5 : c->page_tokens == 64 ? 6 : 7;
+    return ENTRO_OK;
+}
+
+static bool vector_rows(const void *p, int64_t token, int64_t head) { return aligned16(p) && token % 8 == 0 && head % 8 == 0; }
+
+template <typename T, int D>
+static const void *pick_append(int log_page) {
+    switch (log_page) {
+        case 4: return reinterpret_cast<const void *>(append_kernel<T, D, 16>);
+        case 5: return reinterpret_cast<const void *>(append_kernel<T, D, 32>);
+        case 6: return reinterpret_cast<const void *>(append_kernel<T, D, 64>);
+        default: return reinterpret_cast<const void *>(append_kernel<T, D, 128>);
+    }
+}
+
+// f<T, D>() of the cache's type and width
+#define ENTRO_BY_TYPE(c, f, ...)                                                                     \
+    ((c)->type == ENTRO_BF16 ? (c)->head_dim == 64   ? f(__nv_bfloat16, 64, ##__VA_ARGS__)              \
+                               : (c)->head_dim == 96 ? f(__nv_bfloat16, 96, ##__VA_ARGS__)            \
+                                                     : f(__nv_bfloat16, 128, ##__VA_ARGS__)           \
+                             : (c)->head_dim == 64   ? f(__half, 64, ##__VA_ARGS__)                     \
+                               : (c)->head_dim == 96 ? f(__half, 96, ##__VA_ARGS__)                   \
+                                                     : f(__half, 128, ##__VA_ARGS__))
+#define ENTRO_APPEND(T, D, log_page) pick_append<T, D>(log_page)
+#define ENTRO_READ(T, D) reinterpret_cast<const void *>(read_kernel<T, D>)
+#define ENTRO_ATTEND(T, D) reinterpret_cast<const void *>(attend_kernel<T, D>)
+#define ENTRO_JOIN(T, D) reinterpret_cast<const void *>(join_kernel<T, D>)
+
+// CTAs of an attention over the cache: four on each SM.
+static int attend_ctas(int *ctas) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+    DeviceInfo di;
+    const int r = device_info(dev, &di);
+    if (r == ENTRO_OK) *ctas = 4 * di.sms;
+    return r;
+}
+
+}  // namespace entro
+
+using namespace entro;
+
+extern "C" int entro_kv_append(const entro_kv_cache *cache, const void *d_k, int64_t k_token, int64_t k_head, const void *d_v,
+                               int64_t v_token, int64_t v_head, int64_t tokens, const int32_t *d_cu, const int32_t *d_table,
+                               int64_t table_stride, int32_t table_width, const int32_t *d_lens, const int32_t *d_slots,
+                               int32_t batch, int32_t *d_status, void *stream) {
+    AppendArgs a;
+    std::memset(&a, 0, sizeof(a));
+    const int r = make_cache(cache, &a.c);
+    if (r != ENTRO_OK) return r;
+    if (tokens < 0 || tokens > INT32_MAX || batch < 0 || table_width < 0 || table_stride < table_width) return ENTRO_E_INVAL;
+    if (tokens == 0 || batch == 0) return ENTRO_OK;
+    if (!d_k || !d_v || !d_cu || !d_table || !d_lens || !vector_rows(d_k, k_token, k_head) || !vector_rows(d_v, v_token, v_head)) return ENTRO_E_INVAL;
+    if (!d_slots && batch > cache->slots) return ENTRO_E_INVAL;
+    a.in[0] = d_k, a.in[1] = d_v;
+    a.in_token[0] = k_token, a.in_token[1] = v_token, a.in_head[0] = k_head, a.in_head[1] = v_head;
+    a.cu = d_cu, a.table = d_table, a.lens = d_lens, a.slot_of = d_slots, a.status = d_status;
+    a.tokens = tokens, a.table_stride = table_stride, a.batch = batch, a.table_width = table_width;
+    // blocks that get new tokens: each has one at least, and a sequence's n reach at most (n - 2) / P + 2
+    const int P = 1 << a.c.log_page;
+    const int64_t items = std::min<int64_t>(tokens, (tokens + static_cast<int64_t>(batch) * (P - 2)) / P + batch);
+    const void *fn = ENTRO_BY_TYPE(cache, ENTRO_APPEND, a.c.log_page);
+    void *args[] = {&a};
+    const cudaError_t e = launch_ex(fn, dim3(static_cast<unsigned>(items), a.c.kv, 2), kAppendThreads, 0,
+                                    static_cast<cudaStream_t>(stream), 1, false, args);
+    return e == cudaSuccess ? ENTRO_OK : cuda_fail(e, "entro_kv_append");
+}
+
+extern "C" int entro_kv_read(const entro_kv_cache *cache, void *d_k, int64_t k_token, int64_t k_head, void *d_v, int64_t v_token,
+                             int64_t v_head, int64_t tokens, const int32_t *d_cu, const int32_t *d_table, int64_t table_stride,
+                             int32_t table_width, const int32_t *d_slots, int32_t batch, int32_t *d_status, void *stream) {
+    ReadArgs a;
+    std::memset(&a, 0, sizeof(a));
+    const int r = make_cache(cache, &a.c);
+    if (r != ENTRO_OK) return r;
+    if (tokens < 0 || tokens > INT32_MAX || batch < 0 || table_width < 0 || table_stride < table_width) return ENTRO_E_INVAL;
+    if (tokens == 0 || batch == 0) return ENTRO_OK;
+    if (!d_k || !d_v || !d_cu || !d_table || !vector_rows(d_k, k_token, k_head) || !vector_rows(d_v, v_token, v_head)) return ENTRO_E_INVAL;
+    if (!d_slots && batch > cache->slots) return ENTRO_E_INVAL;
+    a.out[0] = d_k, a.out[1] = d_v;
+    a.out_token[0] = k_token, a.out_token[1] = v_token, a.out_head[0] = k_head, a.out_head[1] = v_head;
+    a.cu = d_cu, a.table = d_table, a.slot_of = d_slots, a.status = d_status;
+    a.tokens = tokens, a.table_stride = table_stride, a.batch = batch, a.table_width = table_width;
+    void *args[] = {&a};
+    const cudaError_t e = launch_ex(ENTRO_BY_TYPE(cache, ENTRO_READ), dim3(static_cast<unsigned>((tokens + 7) / 8)), 256, 0,
+                                    static_cast<cudaStream_t>(stream), 1, false, args);
+    return e == cudaSuccess ? ENTRO_OK : cuda_fail(e, "entro_kv_read");
+}
+
+extern "C" int entro_kv_attend_workspace(const entro_kv_cache *cache, uint64_t *bytes) {
+    if (!cache || !bytes) return ENTRO_E_INVAL;
+    int ctas = 0;
+    const int r = attend_ctas(&ctas);
+    if (r == ENTRO_OK) *bytes = static_cast<uint64_t>(ctas) * 2 * kHeads * (cache->head_dim + 2) * 4;
+    return r;
+}
+
+extern "C" int entro_kv_attend(const entro_kv_cache *cache, const void *d_q, int64_t q_token, int64_t q_head, int32_t heads,
+                               const int32_t *d_table, int64_t table_stride, int32_t table_width, const int32_t *d_lens,
+                               const int32_t *d_slots, int32_t batch, float scale, void *d_out, int64_t out_token, int64_t out_head,
+                               void *d_work, uint64_t work_bytes, int32_t *d_status, void *stream) {
+    AttendArgs a;
+    std::memset(&a, 0, sizeof(a));
+    int r = make_cache(cache, &a.c);
+    if (r != ENTRO_OK) return r;
+    if (batch < 0 || heads < 1 || heads % a.c.kv || table_width < 0 || table_stride < table_width || !(scale > 0.0f) || scale > 3.0e38f)
+        return ENTRO_E_INVAL;
+    if (batch == 0) return ENTRO_OK;
+    if (!d_q || !d_out || !d_lens || !d_work || (!d_table && table_width > 0) || !aligned16(d_work) || !vector_rows(d_q, q_token, q_head) ||
+        !vector_rows(d_out, out_token, out_head))
+        return ENTRO_E_INVAL;
+    if (!d_slots && batch > cache->slots) return ENTRO_E_INVAL;
+    r = attend_ctas(&a.ctas);
+    if (r != ENTRO_OK) return r;
+    if (work_bytes < static_cast<uint64_t>(a.ctas) * 2 * kHeads * (cache->head_dim + 2) * 4) return ENTRO_E_INVAL;
+    a.q = d_q, a.out = d_out;
+    a.q_token = q_token, a.q_head = q_head, a.out_token = out_token, a.out_head = out_head;
+    a.table = d_table, a.table_stride = table_stride, a.table_width = table_width;
+    a.lens = d_lens, a.slot_of = d_slots, a.work = static_cast<float *>(d_work), a.status = d_status;
+    a.batch = batch, a.group = heads / a.c.kv, a.chunks = (a.group + kHeads - 1) / kHeads;
+    a.scale_log2 = scale * 1.4426950408889634f;
+    const int64_t columns = static_cast<int64_t>(batch) * a.c.kv * a.chunks;
+    if (columns > INT32_MAX) return ENTRO_E_LIMIT;
+    void *args[] = {&a};
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    cudaError_t e = launch_ex(ENTRO_BY_TYPE(cache, ENTRO_ATTEND), dim3(a.ctas), kAttendThreads, 0, st, 1, false, args);
+    if (e == cudaSuccess)
+        e = launch_ex(ENTRO_BY_TYPE(cache, ENTRO_JOIN), dim3(static_cast<unsigned>(columns)), kAttendThreads, 0, st, 1, columns <= a.ctas, args);
+    return e == cudaSuccess ? ENTRO_OK : cuda_fail(e, "entro_kv_attend");
+}

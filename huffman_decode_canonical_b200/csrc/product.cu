@@ -23,17 +23,6 @@ using namespace sm100;
 
 // ------------------------------------------------------------------ tokens to 8 bits
 
-// 127 x / amax to the nearest whole number, ties to even, exactly: 127 x is
-// exact (at most 18 bits), its product with the rounded reciprocal is off by
-// less than 2^-23 of itself, and a quotient of two numbers of at most 11 bits
-// that is no tie lies at least 2^-19 of itself away from one.  So rounding the
-// product to 20 bits (a split by 2^4 + 1) restores ties and moves nothing else
-// across one.
-__device__ __forceinline__ int code_of(float x127, float rcp) {
-    const float t = __fmul_rn(x127, rcp), c = __fmul_rn(t, 17.0f);
-    return __float2int_rn(__fsub_rn(c, __fsub_rn(c, t)));
-}
-
 struct QuantArgs {
     const uint16_t *x;
     int8_t *q;
@@ -81,34 +70,21 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_kernel(const QuantArgs
     __syncthreads();
     m = 0;
     for (int w = 0; w < kQuantThreads / 32; w++) m = max(m, red_max[w]);
-    const bool finite = m < (Half<T>::kExp & 0xFFFF);
-    const float amax = Half<T>::widen(m).x;
-    // keep products and reciprocal inside the normal range (powers of two: exact)
-    const float pre = amax > 0x1p60f ? 0x1p-64f : amax < 0x1p-60f ? 0x1p64f : 1.0f;
-    const float rcp = finite && amax > 0 ? __frcp_rn(amax * pre) : 0.0f;
-    const float by = finite ? 127.0f * pre : 0.0f;
+    const BlockCode<T> code(m);
     int sum = 0;
-    auto code = [&](float x) { return finite ? code_of(x * by, rcp) : 0; };
     if (VECS) {
 #pragma unroll
         for (int i = 0; i < VECS; i++) {
             const int64_t k = (static_cast<int64_t>(i) * kQuantThreads + tid) * 8;
             if (k >= a.cols) break;
-            const uint32_t e[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-            uint32_t o[2];
-#pragma unroll
-            for (int j = 0; j < 2; j++) {
-                const float2 p = Half<T>::widen(e[2 * j]), r = Half<T>::widen(e[2 * j + 1]);
-                const uint32_t lo = __byte_perm(code(p.x), code(p.y), 0x0040), hi = __byte_perm(code(r.x), code(r.y), 0x0040);
-                o[j] = __byte_perm(lo, hi, 0x5410);
-                sum = __dp4a(static_cast<int>(o[j]), 0x01010101, sum);
-            }
+            const uint2 o = code.eight(v[i]);
+            sum = __dp4a(static_cast<int>(o.x), 0x01010101, __dp4a(static_cast<int>(o.y), 0x01010101, sum));
             // the row pitch is a multiple of 16 bytes: the last vector's zeros fall inside it
-            *reinterpret_cast<uint2 *>(a.q + t * a.ldq + k) = make_uint2(o[0], o[1]);
+            *reinterpret_cast<uint2 *>(a.q + t * a.ldq + k) = o;
         }
     } else {
         for (int64_t k = tid; k < a.cols; k += kQuantThreads) {
-            const int c = code(Half<T>::widen(row[k]).x);
+            const int c = code.one(Half<T>::widen(row[k]).x);
             a.q[t * a.ldq + k] = static_cast<int8_t>(c);
             sum += c;
         }
@@ -120,7 +96,7 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_kernel(const QuantArgs
         sum = 0;
         for (int w = 0; w < kQuantThreads / 32; w++) sum += red_sum[w];
         a.sum[t] = sum;
-        a.scale[t] = finite ? __fdiv_rn(amax, 127.0f) : __int_as_float(0x7FC00000);
+        a.scale[t] = code.scale();
     }
 }
 

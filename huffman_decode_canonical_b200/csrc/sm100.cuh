@@ -275,5 +275,40 @@ struct Half<__half> {
     static constexpr uint32_t kExp = 0x7C007C00u;
 };
 
+// ------------------------------------------------------------------ 8-bit codes
+
+// Codes of numbers that share a scale, from the largest magnitude a among them
+// (top: the bits of that 16-bit float): 127 x / a to the nearest whole number,
+// ties to even, exactly.  127 x is exact (at most 18 bits), its product with the
+// rounded reciprocal is off by less than 2^-23 of itself, and a quotient of two
+// numbers of at most 11 bits that is no tie lies at least 2^-19 of itself away from
+// one.  So rounding the product to 20 bits (a split by 2^4 + 1) restores ties and
+// moves nothing else across one.  All zero: scale 0.  Infinities or NaN among
+// them: scale NaN, codes 0.
+template <typename T>
+struct BlockCode {
+    bool finite;
+    float amax, by, rcp;
+
+    __device__ __forceinline__ explicit BlockCode(uint32_t top) {
+        finite = top < (Half<T>::kExp & 0xFFFF);
+        amax = Half<T>::widen(top).x;
+        // keep products and reciprocal inside the normal range (powers of two: exact)
+        const float pre = amax > 0x1p60f ? 0x1p-64f : amax < 0x1p-60f ? 0x1p64f : 1.0f;
+        rcp = finite && amax > 0 ? __frcp_rn(amax * pre) : 0.0f;
+        by = 127.0f * pre;
+    }
+    __device__ __forceinline__ float scale() const { return finite ? __fdiv_rn(amax, 127.0f) : __int_as_float(0x7FC00000); }
+    __device__ __forceinline__ int one(float x) const {
+        const float t = __fmul_rn(__fmul_rn(x, by), rcp), c = __fmul_rn(t, 17.0f);
+        return finite ? __float2int_rn(__fsub_rn(c, __fsub_rn(c, t))) : 0;
+    }
+    __device__ __forceinline__ uint32_t four(uint32_t lo, uint32_t hi) const {
+        const float2 p = Half<T>::widen(lo), r = Half<T>::widen(hi);
+        return __byte_perm(__byte_perm(one(p.x), one(p.y), 0x0040), __byte_perm(one(r.x), one(r.y), 0x0040), 0x5410);
+    }
+    __device__ __forceinline__ uint2 eight(uint4 v) const { return make_uint2(four(v.x, v.y), four(v.z, v.w)); }
+};
+
 }  // namespace sm100
 }  // namespace entro

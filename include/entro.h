@@ -272,6 +272,68 @@ ENTRO_API int entro_matmul_i8(const int8_t *d_q, int64_t ldq, const float *d_x_s
                               const float *d_w_scale, float w_scale, const int32_t *d_w_zero, int32_t w_zero, void *d_y,
                               int32_t y_type, int64_t ldy, int32_t *d_status, void *stream);
 
+/* A key/value cache in 8 bits, in pages of page_tokens tokens.  A page and key
+ * head share a scale (one for keys, one for values): a full block of tokens is
+ * held as codes 127 x / a (nearest, ties to even; a the block's and head's
+ * largest magnitude) with scale a / 127, or scale NaN and codes 0 if one of its
+ * numbers is infinite or NaN.  The tokens of a sequence's last block, until it is
+ * full, are held as they are in the sequence's tail slot.  So the cache of a
+ * sequence is the same however its tokens arrived.  All buffers are the caller's,
+ * contiguous and 16-byte aligned; nothing in them has to be initialised.  A page
+ * may belong to several sequences that only read it; a tail slot belongs to one
+ * sequence.  One cache serves one layer. */
+typedef struct entro_kv_cache {
+    void *k_codes, *v_codes; /* int8 [pages][kv_heads][page_tokens][head_dim] */
+    void *k_scale, *v_scale; /* fp32 [pages][kv_heads] */
+    void *k_tail, *v_tail;   /* type [slots][kv_heads][page_tokens][head_dim] */
+    int64_t pages, slots;
+    int32_t kv_heads;
+    int32_t page_tokens;     /* 16, 32, 64 or 128 */
+    int32_t head_dim;        /* 64, 96 or 128 */
+    int32_t type;            /* ENTRO_BF16 or ENTRO_F16: keys, values and queries */
+} entro_kv_cache;
+
+/* Arguments that the cache's calls share: d_table int32 [batch][table_width] with
+ * rows table_stride apart, the pages of each sequence's blocks in order (entries
+ * past its full blocks are not read); d_lens int32 [batch], each sequence's
+ * tokens; d_cu int32 [batch + 1], where each sequence's tokens begin among packed
+ * ones; d_slots int32 [batch], each sequence's tail slot (NULL: slot b for
+ * sequence b).  Keys, values, queries and outputs are [tokens or batch][heads]
+ * [head_dim] with adjacent channels and any strides (elements) that are multiples
+ * of 8, on 16-byte aligned buffers.  Lengths, pages and slots are read on the
+ * device; one that is out of range is reported as ENTRO_E_INVAL in *d_status, and
+ * what it names is neither read nor written. */
+
+/* Append packed new tokens to their sequences: d_lens counts them already.
+ * Blocks that fill up are coded into their pages, the rest goes to the tail.  No
+ * page or slot may be given twice for writing. */
+ENTRO_API int entro_kv_append(const entro_kv_cache *cache, const void *d_k, int64_t k_token, int64_t k_head, const void *d_v,
+                              int64_t v_token, int64_t v_head, int64_t tokens, const int32_t *d_cu, const int32_t *d_table,
+                              int64_t table_stride, int32_t table_width, const int32_t *d_lens, const int32_t *d_slots,
+                              int32_t batch, int32_t *d_status, void *stream);
+
+/* All tokens of the sequences back, packed: code times scale, rounded once;
+ * sequence b holds d_cu[b+1] - d_cu[b] tokens (for the attention of a prompt's
+ * next part over what is cached).  Tokens of no sequence are left as they are. */
+ENTRO_API int entro_kv_read(const entro_kv_cache *cache, void *d_k, int64_t k_token, int64_t k_head, void *d_v, int64_t v_token,
+                            int64_t v_head, int64_t tokens, const int32_t *d_cu, const int32_t *d_table, int64_t table_stride,
+                            int32_t table_width, const int32_t *d_slots, int32_t batch, int32_t *d_status, void *stream);
+
+/* Attention of one token of each sequence over its cache: for b < batch and
+ * h < heads (a multiple of kv_heads; head h reads key head h / (heads / kv_heads)),
+ *   out[b,h] = sum_j p_j v_j,  p = softmax_j(scale q[b,h] . k_j),  j < d_lens[b]
+ * over the values that the cache stands for.  A sequence without tokens gets 0.
+ * Scores, sums and outputs are taken in fp32, the weights p rounded to fp16; a
+ * result does not depend on when it is computed (no atomics), but on the batch,
+ * which decides how the work is split.  scale > 0.  d_work: device memory of at
+ * least entro_kv_attend_workspace bytes, 16-byte aligned, of this call alone until
+ * it has run. */
+ENTRO_API int entro_kv_attend_workspace(const entro_kv_cache *cache, uint64_t *bytes);
+ENTRO_API int entro_kv_attend(const entro_kv_cache *cache, const void *d_q, int64_t q_token, int64_t q_head, int32_t heads,
+                              const int32_t *d_table, int64_t table_stride, int32_t table_width, const int32_t *d_lens,
+                              const int32_t *d_slots, int32_t batch, float scale, void *d_out, int64_t out_token,
+                              int64_t out_head, void *d_work, uint64_t work_bytes, int32_t *d_status, void *stream);
+
 /* Launch overlap (not in the pages: a B200 launch option).  When enabled,
  * decode launches that fill each SM with one or two large CTAs (the lanes-
  * format kernels on tensors large enough for it) are made with programmatic

@@ -46,7 +46,7 @@ def _expect(xq, w, w_scale, w_zero):
 
 
 def _close(y, want):
-    half = {torch.float32: 0.0, torch.bfloat16: 2.0 ** -9 * 2, torch.float16: 2.0 ** -11}[y.dtype]
+    half = {torch.float32: 0.0, torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11}[y.dtype]
     got, bound = y.cpu().double().numpy(), np.abs(want) * (3.01 * 2.0 ** -24 + half)
     if y.dtype == torch.float16:
         bound = bound + 2.0 ** -25  # half a step of its smallest numbers
