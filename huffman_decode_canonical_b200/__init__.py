@@ -70,7 +70,7 @@ EXPORTS = ["entro_encode", "entro_blob_from_bytes", "entro_blob_bytes", "entro_b
            "entro_group_launch", "entro_group_free", "entro_strerror", "entro_version", "entro_last_cuda_error",
            "entro_decode_gemv_group_static", "entro_set_overlap", "entro_test_stall_tables",
            "entro_quantize_tokens", "entro_unpack_codes", "entro_matmul_i8",
-           "entro_kv_append", "entro_kv_read", "entro_kv_attend_workspace", "entro_kv_attend"]
+           "entro_kv_append", "entro_kv_read", "entro_kv_attend_workspace", "entro_kv_attend", "entro_attention_prompt"]
 
 
 def _load() -> ctypes.CDLL:
@@ -107,6 +107,8 @@ def _load() -> ctypes.CDLL:
         "entro_kv_read": ([P, P, I64, I64, P, I64, I64, I64, P, P, I64, I32, P, I32, P, P], I32),
         "entro_kv_attend_workspace": ([P, ctypes.POINTER(U64)], I32),
         "entro_kv_attend": ([P, P, I64, I64, I32, P, I64, I32, P, P, I32, F32, P, I64, I64, P, U64, P, P], I32),
+        "entro_attention_prompt": ([I32, I32, P, I64, I64, I32, I64, P, I64, I64, P, I64, I64, I32, I64, P, P, I32, F32, P, I64,
+                                    I64, P, P], I32),
         "entro_quantize_tokens": ([P, I32, I64, I64, I64, P, I64, P, P, P], I32),
         "entro_unpack_codes": ([P, I32, I64, I64, P, I64, P], I32),
         "entro_matmul_i8": ([P, I64, P, P, I64, P, I32, I64, I64, I64, P, F32, P, I32, P, I32, I64, P, P], I32),
@@ -499,6 +501,55 @@ def _index(t: torch.Tensor, name: str, shape: tuple):
         raise ValueError(f"{name} must be a contiguous int32 {list(shape)} tensor")
 
 
+def attention_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor,
+                     cu_keys: Optional[torch.Tensor] = None, scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
+                     status: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """Causal attention over packed prompts: q [tokens, heads, head_dim], k and v [keys, kv_heads, head_dim], bf16 or
+    fp16 (slices of one projection's output as they are).  cu_seqlens int32 [batch + 1] says where each sequence's queries
+    begin, cu_keys its keys (None: as the queries); a sequence's last query sees its last key, so queries that continue a
+    context give their keys with it.  scale: 1 / sqrt(head_dim) by default.  Rows of no sequence are left as they are (give
+    `out` to keep theirs)."""
+    if q.dtype not in (torch.bfloat16, torch.float16) or q.dim() != 3 or k.dim() != 3:
+        raise ValueError("q, k and v must be bf16 or fp16 [tokens, heads, head_dim] tensors")
+    tokens, heads, dim = q.shape
+    keys, kv = k.shape[:2]
+    if dim not in (64, 96, 128):
+        raise ValueError("head_dim must be 64, 96 or 128")
+    if kv < 1 or heads < 1 or heads % kv:
+        raise ValueError("q's heads must be a multiple of k's")
+    _rows(q, "q", q.dtype, heads, dim)
+    _rows(k, "k", q.dtype, kv, dim)
+    _rows(v, "v", q.dtype, kv, dim)
+    if v.shape[0] != keys:
+        raise ValueError("k and v must have the same number of tokens")
+    for t, name in ((q, "q"), (k, "k"), (v, "v")):
+        if (t.shape[0] > 1 and t.stride(0) == 0) or (t.shape[1] > 1 and t.stride(1) == 0):
+            raise ValueError(f"{name} must not be expanded")
+    batch = cu_seqlens.shape[0] - 1 if cu_seqlens.dim() == 1 else -1
+    if batch < 0:
+        raise ValueError("cu_seqlens must be an int32 [batch + 1] tensor")
+    _index(cu_seqlens, "cu_seqlens", (batch + 1,))
+    if cu_keys is not None:
+        _index(cu_keys, "cu_keys", (batch + 1,))
+    elif keys != tokens:
+        raise ValueError("without cu_keys, k and v must have q's tokens")
+    if out is not None:
+        _rows(out, "out", q.dtype, heads, dim)
+        if out.shape[0] != tokens:
+            raise ValueError("out must have q's shape")
+    scale = dim ** -0.5 if scale is None else float(scale)
+    if not 0.0 < scale < 3e38:
+        raise ValueError("scale must be above 0 and finite")
+    _inputs(q.device, q=q, k=k, v=v, cu_seqlens=cu_seqlens, cu_keys=cu_keys, out=out, status=status)
+    with _on(q.device, stream) as s:
+        out = torch.empty((tokens, heads, dim), dtype=q.dtype, device=q.device) if out is None else out
+        _check(_lib.entro_attention_prompt(_TYPES[q.dtype], dim, q.data_ptr(), *_strides(q), heads, tokens, k.data_ptr(), *_strides(k),
+                                           v.data_ptr(), *_strides(v), kv, keys, cu_seqlens.data_ptr(),
+                                           cu_keys.data_ptr() if cu_keys is not None else None, batch, scale, out.data_ptr(),
+                                           *_strides(out), _dptr(status), s), "entro_attention_prompt")
+    return out
+
+
 class KVCache:
     """Keys and values of one layer in 8 bits, in pages with a scale for each page and head (`entro_kv_cache`).
 
@@ -650,7 +701,7 @@ def set_overlap(enable: bool) -> bool:
 
 
 __all__ = ["Blob", "DeviceTensor", "Group", "EntroError", "encode", "upload", "lib", "version", "set_overlap", "EXPORTS",
-           "decode_gemv_group_static", "STATIC_GROUP_MAX", "QuantTokens", "quantize_tokens", "matmul_i8", "KVCache",
+           "decode_gemv_group_static", "STATIC_GROUP_MAX", "QuantTokens", "quantize_tokens", "matmul_i8", "attention_prompt", "KVCache",
            "test_stall_tables", "QUANT_AUTO", "QUANT_UNSIGNED", "QUANT_ASYM", "FORMAT_SINGLE", "FORMAT_LANES", "FORMAT_ROWS_CO",
            "FORMAT_ROWS", "GROUP_GEMV",
            "GROUP_BF16", "SCHEME_UNSIGNED", "SCHEME_ASYM"]

@@ -19,7 +19,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libentro.so")
 OBJECTS = os.path.join(HERE, "_build")
-SOURCES = [os.path.join(CSRC, f) for f in ("decode.cu", "product.cu", "kvcache.cu", "encoder.cpp", "launch.cpp")]
+SOURCES = [os.path.join(CSRC, f) for f in ("decode.cu", "product.cu", "prompt.cu", "kvcache.cu", "encoder.cpp", "launch.cpp")]
 HEADERS = sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".h", ".cuh"))) + [
     os.path.join(ROOT, "include", "entro.h")]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")

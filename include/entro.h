@@ -272,6 +272,27 @@ ENTRO_API int entro_matmul_i8(const int8_t *d_q, int64_t ldq, const float *d_x_s
                               const float *d_w_scale, float w_scale, const int32_t *d_w_zero, int32_t w_zero, void *d_y,
                               int32_t y_type, int64_t ldy, int32_t *d_status, void *stream);
 
+/* Causal attention over packed prompts with grouped heads.  q [tokens][heads]
+ * [head_dim], k and v [keys][kv_heads][head_dim] and out like q, of type ENTRO_BF16
+ * or ENTRO_F16, head_dim 64, 96 or 128, adjacent channels, strides in elements that
+ * are multiples of 8 (of q, k and v above 0), on 16-byte aligned buffers: the parts
+ * of one projection's output as they are.  Sequence b's queries are rows d_cu_q[b]
+ * to d_cu_q[b+1] (int32 [batch + 1], device), its keys those of d_cu_k (NULL: the
+ * same as the queries, tokens == keys).  Its last query sees its last key: query i
+ * sees keys j <= i + klen - qlen, so a prompt's next part attends to what came
+ * before it.  Head h reads key head h / (heads / kv_heads).
+ *   out[i,h] = sum_j p_j v_j,  p = softmax_j(scale q[i,h] . k_j),  scale > 0
+ * A query that sees no key gets 0; rows of no sequence are left as they are; what
+ * the mask hides does not count, infinities and NaN included.  Scores, sums and
+ * outputs are taken in fp32, the weights p rounded to `type`; results do not
+ * depend on the other sequences of the batch.  Offsets out of range are reported
+ * as ENTRO_E_INVAL in *d_status and their sequence is skipped. */
+ENTRO_API int entro_attention_prompt(int32_t type, int32_t head_dim, const void *d_q, int64_t q_token, int64_t q_head,
+                                     int32_t heads, int64_t tokens, const void *d_k, int64_t k_token, int64_t k_head,
+                                     const void *d_v, int64_t v_token, int64_t v_head, int32_t kv_heads, int64_t keys,
+                                     const int32_t *d_cu_q, const int32_t *d_cu_k, int32_t batch, float scale, void *d_out,
+                                     int64_t out_token, int64_t out_head, int32_t *d_status, void *stream);
+
 /* A key/value cache in 8 bits, in pages of page_tokens tokens.  A page and key
  * head share a scale (one for keys, one for values): a full block of tokens is
  * held as codes 127 x / a (nearest, ties to even; a the block's and head's
