@@ -40,17 +40,24 @@ struct PromptArgs {
     uint32_t tx_extra;
 };
 
-constexpr int kRows = 128;             // rows of a query tile, and of a key tile
-constexpr int kChunk = kRows * 128;    // bytes of 128 rows of 64 channels (one TMA box)
-constexpr int kPromptThreads = 384;    // 2 x 4 softmax warps, MMA, copies, 2 warps that look over values
+constexpr int kRows = 128;             // rows of a query tile
+constexpr int kPromptThreads = 384;    // 2 x 4 softmax warps, an MMA warp for each query tile, copies, a look over values
 constexpr float kLazyLog2 = 8.0f;
+constexpr int kMarks = 8;              // barriers for masked value tiles, more than the ring holds
 
+// TMEM has 512 columns: two query tiles' scores (a column a key), weights (two keys a column) and outputs (a column a
+// channel).  With weights of their own the next scores do not wait for the last weights' product, so the softmax
+// warps always find scores ready; 128 keys leave room for that beside outputs of 64 channels, 96 beside 96, 64 beside 128.
 template <int D>
 struct PromptShape {
-    static constexpr int kChunks = (D + 63) / 64;              // 96 channels fill one and a half; the rest reads as zero
-    static constexpr int kTileBytes = kChunks * kChunk;
-    static constexpr int kStages = D == 64 ? 8 : 4;            // key and value tiles in flight
-    static constexpr int kSmem = 1024 + (2 + kStages) * kTileBytes;
+    static constexpr int kKeys = D == 64 ? 128 : D == 96 ? 96 : 64;  // keys of a tile
+    static constexpr int kChunks = (D + 63) / 64;              // 64 channels each; 96 fill one and a half, the rest reads as zero
+    static constexpr int kQChunk = kRows * 128, kChunk = kKeys * 128;  // bytes of a chunk (one TMA box)
+    static constexpr int kQTile = kChunks * kQChunk, kTile = kChunks * kChunk;
+    static constexpr int kStages = (220 * 1024 - 2 * kQTile) / kTile < 10 ? (220 * 1024 - 2 * kQTile) / kTile : 10;  // key and value tiles in flight
+    static constexpr int kSmem = 1024 + 2 * kQTile + kStages * kTile;
+    static constexpr uint32_t kS = 0, kP = 2 * kKeys, kO = 3 * kKeys;  // TMEM columns: S0 S1 P0 P1 O0 O1
+    static_assert(kO + 2 * D <= 512 && kStages / 2 < kMarks && kStages >= 4 && kKeys % 32 == 0, "");
 };
 
 __device__ __forceinline__ float exp2_fast(float x) {
@@ -59,10 +66,38 @@ __device__ __forceinline__ float exp2_fast(float x) {
     return y;
 }
 
+// Pairs of fp32 numbers in one instruction.
+__device__ __forceinline__ uint64_t pair(uint32_t lo, uint32_t hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+    return r;
+}
+__device__ __forceinline__ uint64_t pair(float lo, float hi) { return pair(__float_as_uint(lo), __float_as_uint(hi)); }
+__device__ __forceinline__ float2 halves(uint64_t v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
 // One row by the definition, by one warp: for rows whose tile holds an infinity
 // or NaN among values that other rows do not see.
 template <typename T, int D>
-__device__ __noinline__ void row_by_row(const PromptArgs &a, int head, int64_t q_row, int64_t k_row, int visible) {
+__device__ __forceinline__ void row_by_row(const PromptArgs &a, int head, int64_t q_row, int64_t k_row, int visible) {
     const int lane = threadIdx.x % 32;
     const T *q = static_cast<const T *>(a.q) + q_row * a.q_token + head * a.q_head;
     const T *k = static_cast<const T *>(a.k) + k_row * a.k_token + (head / a.group) * a.k_head;
@@ -107,286 +142,442 @@ __device__ __noinline__ void row_by_row(const PromptArgs &a, int head, int64_t q
     for (int i = 0; i < D / 32; i++) out[i * 32 + lane] = static_cast<T>(l == 0.0f ? 0.0f : o[i] / l);
 }
 
+// What a CTA works on: 256 queries of a head.
+struct PromptItem {
+    int q0, qlen, k0, klen, row0, head;  // head < 0: no more work
+
+    __device__ __forceinline__ int offset() const { return klen - qlen; }  // query i sees keys up to i + offset
+    // key tiles of query tile t (0: no rows, or none that sees a key)
+    template <int KEYS>
+    __device__ __forceinline__ int key_tiles(int t) const {
+        const int first = row0 + t * kRows;
+        if (first >= qlen) return 0;
+        const int64_t most = static_cast<int64_t>(min(first + kRows, qlen)) + offset();
+        return most <= 0 ? 0 : static_cast<int>((most + KEYS - 1) / KEYS);
+    }
+    // key tiles from here on hold keys that some row must not see
+    template <int KEYS>
+    __device__ __forceinline__ int masked_from() const { return offset() + row0 + 1 <= 0 ? 0 : (offset() + row0 + 1) / KEYS; }
+};
+
+// Block number -> item, by a warp: heads fastest, so that those of a key head meet in L2; of a sequence's blocks the
+// last first, since it has most keys.  False: a block of no item (the grid is cut for the most there may be).
+__device__ __forceinline__ bool find_item(const PromptArgs &a, int block, PromptItem &it) {
+    const int lane = threadIdx.x % 32;
+    it.head = block % a.heads;
+    int left = block / a.heads;
+    for (int b0 = 0; b0 < a.batch; b0 += 32) {
+        const int b = b0 + lane;
+        int q0 = 0, qn = 0, k0 = 0, kn = 0;
+        if (b < a.batch) {
+            q0 = a.cu_q[b], qn = a.cu_q[b + 1] - q0;
+            k0 = a.cu_k[b], kn = a.cu_k[b + 1] - k0;
+            if (q0 < 0 || qn < 0 || static_cast<int64_t>(q0) + qn > a.tokens || k0 < 0 || kn < 0 ||
+                static_cast<int64_t>(k0) + kn > a.keys) {
+                set_status(a.status, ENTRO_E_INVAL);
+                qn = 0;
+            }
+        }
+        const int blocks = qn / 256 + (qn % 256 != 0);
+        int sum = blocks;
+        for (int o = 1; o < 32; o *= 2) {
+            const int up = __shfl_up_sync(~0u, sum, o);
+            if (lane >= o) sum += up;
+        }
+        const uint32_t here = __ballot_sync(~0u, left < sum);
+        if (here) {
+            const int from = __ffs(here) - 1;
+            it.q0 = __shfl_sync(~0u, q0, from), it.qlen = __shfl_sync(~0u, qn, from);
+            it.k0 = __shfl_sync(~0u, k0, from), it.klen = __shfl_sync(~0u, kn, from);
+            it.row0 = (__shfl_sync(~0u, sum, from) - 1 - left) * 256;
+            return true;
+        }
+        left -= __shfl_sync(~0u, sum, 31);
+    }
+    return false;
+}
+
+// The next block that has not started, in place of which this CTA goes on (cluster launch control).
+__device__ __forceinline__ void ask_next(uint32_t reply, uint32_t bar) {
+    bar_expect(bar, 16);
+    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(reply), "r"(bar)
+                 : "memory");
+}
+__device__ __forceinline__ int next_block(uint32_t reply) {  // -1: none is left
+    uint32_t x;
+    asm volatile(
+        "{\n\t.reg .b128 r;\n\t.reg .pred p;\n\t"
+        "ld.shared.b128 r, [%1];\n\t"
+        "mov.u32 %0, 0xffffffff;\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %0, r;\n\t}"
+        : "=r"(x)
+        : "r"(reply)
+        : "memory");
+    fence_async_smem();  // read before the next reply is written
+    return static_cast<int>(x);
+}
+
 template <typename T, int D>
 __global__ void __launch_bounds__(kPromptThreads, 1)
     prompt_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
                   const __grid_constant__ CUtensorMap v_map, const __grid_constant__ PromptArgs a) {
     using Shape = PromptShape<D>;
-    constexpr int kStages = Shape::kStages;
+    constexpr int kStages = Shape::kStages, kKeys = Shape::kKeys;
     // weights are held as 2^6 times theirs in fp16: at most 2^14, and none above 2^-30 of the largest is lost
     constexpr float kBias = Half<T>::kExp == 0x7C007C00u ? 6.0f : 0.0f;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ __align__(8) uint64_t bars[2 * kStages + 1 + 2 + 2 + 2 + 3 + 3];
+    __shared__ __align__(16) uint32_t reply[4];
+    __shared__ PromptItem items[2];
+    __shared__ __align__(8) uint64_t bars[2 * kStages + 21 + 2 * kMarks];
     __shared__ uint32_t tmem_base;
-    __shared__ int failed, special, where[6];
-    const uint32_t base = (smem_u32(smem_raw) + 1023) & ~1023u, ring = base + 2 * Shape::kTileBytes;
+    __shared__ int failed, special[4];
+    const uint32_t base = (smem_u32(smem_raw) + 1023) & ~1023u, ring = base + 2 * Shape::kQTile;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-    const uint32_t full = smem_u32(bars), empty = full + 8 * kStages, q_full = empty + 8 * kStages, s_full = q_full + 8,
-                   p_full = s_full + 16, o_full = p_full + 16, v_sent = o_full + 16, v_seen = v_sent + 24;
-
-    // this CTA's query tiles: (sequence, block of 256 queries), the last block of a sequence first, since it has most keys
-    const int head = blockIdx.x % a.heads;
+    // Barriers, each with a count of its own that goes on from item to item:
+    const uint32_t full = smem_u32(bars), empty = full + 8 * kStages;       // key and value tiles
+    const uint32_t item_full = empty + 8 * kStages, item_empty = item_full + 16;  // item n in place n % 2
+    const uint32_t q_full = item_empty + 16, q_empty = q_full + 8;          // the item's queries; (per tile) read for the last time
+    const uint32_t s_full = q_empty + 16, s_read = s_full + 16;             // per tile: scores; taken into registers
+    const uint32_t p_full = s_read + 16, p_read = p_full + 16;              // per tile: weights; multiplied
+    const uint32_t o_full = p_read + 16, o_empty = o_full + 16;             // per tile: the item's output; stored
+    const uint32_t asked = o_empty + 16, turn = asked + 8, v_sent = turn + 8, v_seen = v_sent + 8 * kMarks;  // masked value tile g in place g % kMarks: on its way; looked over
     if (warp == 0) {
-        int64_t item = blockIdx.x / a.heads;
-        if (lane == 0) where[0] = -1;
-        __syncwarp();
-        for (int b0 = 0; b0 < a.batch; b0 += 32) {
-            const int b = b0 + lane;
-            int q0 = 0, qn = 0, k0 = 0, kn = 0;
-            if (b < a.batch) {
-                q0 = a.cu_q[b], qn = a.cu_q[b + 1] - q0;
-                k0 = a.cu_k[b], kn = a.cu_k[b + 1] - k0;
-                if (q0 < 0 || qn < 0 || static_cast<int64_t>(q0) + qn > a.tokens || k0 < 0 || kn < 0 ||
-                    static_cast<int64_t>(k0) + kn > a.keys) {
-                    set_status(a.status, ENTRO_E_INVAL);
-                    qn = 0;
-                }
+        if (lane == 0) {
+            for (int s = 0; s < kStages; s++) {
+                bar_init(full + 8 * s, 1);
+                bar_init(empty + 8 * s, 2);
             }
-            const int blocks = qn / 256 + (qn % 256 != 0);
-            int sum = blocks;
-            for (int o = 1; o < 32; o *= 2) {
-                const int up = __shfl_up_sync(~0u, sum, o);
-                if (lane >= o) sum += up;
+            bar_init(q_full, 1);
+            bar_init(asked, 1);
+            bar_init(turn, 4);
+            for (int t = 0; t < 2; t++) {
+                bar_init(item_full + 8 * t, 1);
+                bar_init(item_empty + 8 * t, 11);  // two MMA warps, the look-over, eight softmax warps
+                bar_init(q_empty + 8 * t, 1);
+                bar_init(s_full + 8 * t, 1);
+                bar_init(s_read + 8 * t, 4);
+                bar_init(p_full + 8 * t, 4);
+                bar_init(p_read + 8 * t, 1);
+                bar_init(o_full + 8 * t, 1);
+                bar_init(o_empty + 8 * t, 4);
             }
-            if (item < sum && item >= sum - blocks) {
-                where[0] = q0, where[1] = qn, where[2] = k0, where[3] = kn;
-                where[4] = sum - 1 - static_cast<int>(item);
+            for (int j = 0; j < kMarks; j++) {
+                bar_init(v_sent + 8 * j, 1);
+                bar_init(v_seen + 8 * j, 1);
             }
-            const int all = __shfl_sync(~0u, sum, 31);
-            if (item < all) break;
-            item -= all;
+            fence_bar_init();
+            failed = special[0] = special[1] = special[2] = special[3] = 0;
         }
     } else if (warp == 1 && lane == 0) {
-        for (int s = 0; s < kStages; s++) {
-            bar_init(full + 8 * s, 1);
-            bar_init(empty + 8 * s, 1);
-        }
-        bar_init(q_full, 1);
-        for (int t = 0; t < 2; t++) {
-            bar_init(s_full + 8 * t, 1);
-            bar_init(p_full + 8 * t, 4);
-            bar_init(o_full + 8 * t, 1);
-        }
-        for (int j = 0; j < 3; j++) {
-            bar_init(v_sent + 8 * j, 1);
-            bar_init(v_seen + 8 * j, 2);
-        }
-        fence_bar_init();
-        failed = special = 0;
         prefetch_map(&q_map);
         prefetch_map(&k_map);
         prefetch_map(&v_map);
+    } else if (warp == 8) {
+        tmem_alloc<1>(smem_u32(&tmem_base), 512);
     }
-    __syncthreads();
-    if (where[0] < 0) return;  // (the grid has a few more blocks than there may be query tiles)
-    if (warp == 8) tmem_alloc<1>(smem_u32(&tmem_base), 512);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_base;
-    const int q0 = where[0], qlen = where[1], k0 = where[2], klen = where[3], row0 = where[4] * 256;
-    const int offset = klen - qlen;  // query i sees keys up to i + offset
-    // key tiles of each query tile (0: no rows, or none that sees a key)
-    auto key_tiles = [&](int t) {
-        const int first = row0 + t * kRows;
-        if (first >= qlen) return 0;
-        const int64_t most = static_cast<int64_t>(min(first + kRows, qlen)) + offset;
-        return most <= 0 ? 0 : static_cast<int>((most + kRows - 1) / kRows);
-    };
-    const int n0 = key_tiles(0), n1 = key_tiles(1), n = max(n0, n1);
-    // key tiles from here on (three at most) hold keys that some row of the CTA must not see
-    const int masked_from = offset + row0 + 1 <= 0 ? 0 : (offset + row0 + 1) / kRows;
     bool ok = true;
+    // item n as the other warps take it from its place; every lane waits, so that a warp leaves together
+    auto take = [&](int n, PromptItem &it) {
+        if (!__all_sync(~0u, bar_wait(item_full + 8 * (n % 2), n / 2 & 1))) {
+            ok = false;
+            return false;
+        }
+        it = items[n % 2];
+        __syncwarp();
+        if (lane == 0) bar_arrive(item_empty + 8 * (n % 2));
+        return it.head >= 0;
+    };
 
-    if (warp == 9) {
-        // ---- copies: queries, then K0 V0 K1 V1 ...
-        if (elect_one() && n > 0) {
-            const int kv = head / a.group;
-            bar_expect(q_full, (n1 > 0 ? 2 : 1) * Shape::kTileBytes + a.tx_extra);
-            for (int t = 0; t < (n1 > 0 ? 2 : 1); t++)
-                for (int c = 0; c < Shape::kChunks; c++)
-                    tma_3d(base + t * Shape::kTileBytes + c * kChunk, &q_map, q_full, c * 64, head, q0 + row0 + t * kRows);
-            for (int i = 0; i < 2 * n; i++) {
-                const int s = i % kStages, round = i / kStages;
-                if (round > 0 && !bar_wait(empty + 8 * s, (round - 1) & 1)) {
-                    ok = false;
-                    break;
-                }
-                bar_expect(full + 8 * s, Shape::kTileBytes);
-                for (int c = 0; c < Shape::kChunks; c++)
-                    tma_3d(ring + s * Shape::kTileBytes + c * kChunk, i % 2 ? &v_map : &k_map, full + 8 * s, c * 64, kv, k0 + i / 2 * kRows);
-                // from here on the tile's barrier is in the phase that the warps below wait for
-                if (i % 2 && i / 2 >= masked_from) bar_arrive(v_sent + 8 * (i / 2 - masked_from));
-            }
-        }
-    } else if (warp == 8) {
-        // ---- MMAs
-        if (elect_one() && n > 0) {
-            constexpr uint32_t kScores = kAccF32 | Half<T>::kA | Half<T>::kB | mma_shape(kRows, kRows);
-            constexpr uint32_t kValues = kAccF32 | Half<T>::kA | Half<T>::kB | kBMajorMN | mma_shape(kRows, D);
-            auto scores = [&](int t, int i) {  // S_t = Q_t K^T, with K in ring place i
-                const uint32_t qa = base + t * Shape::kTileBytes, ka = ring + i % kStages * Shape::kTileBytes;
-#pragma unroll
-                for (int k = 0; k < D / 16; k++) {
-                    const uint32_t at = k / 4 * kChunk + k % 4 * 32;
-                    mma_f16(tmem + t * kRows, operand_desc(qa + at, 16, 1024), operand_desc(ka + at, 16, 1024), kScores, k > 0);
-                }
-                mma_commit(s_full + 8 * t);
-            };
-            auto arrived = [&](int i) { return bar_wait(full + 8 * (i % kStages), i / kStages & 1); };
-            do {
-                if (!(ok = bar_wait(q_full, 0) && arrived(0))) break;
-                tc_fence_after();
-                if (n0 > 0) scores(0, 0);
-                if (n1 > 0) scores(1, 0);
-                mma_commit(empty);
-                for (int j = 0; j < n && ok; j++) {
-                    const int iv = 2 * j + 1, ik = 2 * j + 2;
-                    if (!(ok = arrived(iv))) break;
-                    if (j >= masked_from && !(ok = bar_wait(v_seen + 8 * (j - masked_from), 0))) break;
-                    if (j + 1 < n && !(ok = arrived(ik))) break;
-                    for (int t = 0; t < 2; t++) {
-                        const int nt = t ? n1 : n0;
-                        if (j >= nt) continue;
-                        if (!(ok = bar_wait(p_full + 8 * t, j & 1))) break;
-                        tc_fence_after();
-                        const uint32_t va = ring + iv % kStages * Shape::kTileBytes;
-#pragma unroll
-                        for (int k = 0; k < kRows / 16; k++)
-                            mma_f16_ta(tmem + 2 * kRows + t * 128, tmem + t * kRows + k * 8, operand_desc(va + k * 2048, kChunk, 1024),
-                                       kValues, j > 0 || k > 0);
-                        // (MMAs run in order: the next scores overwrite P after it has been read)
-                        if (j + 1 < nt) scores(t, ik);
-                        else mma_commit(o_full + 8 * t);
-                    }
+    // registers: a softmax thread holds a row of scores (the shares add up to the launch's 384 x 168)
+    if (warp >= 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        if (warp == 10) {
+            // ---- items and copies: queries, then K0 V0 K1 V1 ...
+            int block = blockIdx.x, items_out = 0, queries = 0, i = 0, g = 0, answers = 0;
+            PromptItem it;
+            while (ok) {
+                const bool is = block >= 0 && find_item(a, block, it);
+                if (is || block < 0) {
+                    if (block < 0) it.head = -1;
+                    if (items_out >= 2) ok = __all_sync(~0u, bar_wait(item_empty + 8 * (items_out % 2), (items_out / 2 - 1) & 1));
                     if (!ok) break;
-                    mma_commit(empty + 8 * (iv % kStages));
-                    if (j + 1 < n) mma_commit(empty + 8 * (ik % kStages));
-                }
-            } while (false);
-        }
-    } else if (warp >= 10) {
-        // ---- values that some row must not see
-        for (int j = masked_from; j < n; j++) {
-            const int i = 2 * j + 1;
-            if (!bar_wait(v_sent + 8 * (j - masked_from), 0) || !bar_wait(full + 8 * (i % kStages), i / kStages & 1)) {
-                ok = false;
-                break;
-            }
-            const uint32_t tile = ring + i % kStages * Shape::kTileBytes;
-            bool odd = false;
-            for (int u = tid - 320; u < Shape::kTileBytes / 16; u += 64) {
-                // (the swizzle moves 16-byte pieces inside a row of 128 bytes only)
-                const int key = j * kRows + u % (kChunk / 16) / 8;
-                if (key >= klen) {
-                    asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(tile + u * 16), "r"(0) : "memory");
-                } else {
-                    uint32_t x[4];
-                    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]) : "r"(tile + u * 16));
-#pragma unroll
-                    for (int w = 0; w < 4; w++) {
-                        constexpr uint32_t kLow = Half<T>::kExp & 0xFFFF, kHigh = Half<T>::kExp & 0xFFFF0000u;
-                        odd = odd || (x[w] & kLow) == kLow || (x[w] & kHigh) == kHigh;
+                    if (lane == 0) {
+                        items[items_out % 2] = it;
+                        bar_arrive(item_full + 8 * (items_out % 2));
+                    }
+                    items_out++;
+                    if (block < 0) break;
+                    const int n1 = it.key_tiles<kKeys>(1), n = max(it.key_tiles<kKeys>(0), n1), masked_from = it.masked_from<kKeys>();
+                    if (n > 0) {
+                        if (elect_one()) {
+                            const int kv = it.head / a.group, tiles = n1 > 0 ? 2 : 1;
+                            for (int t = 0; t < 2 && queries > 0 && ok; t++) ok = bar_wait(q_empty + 8 * t, (queries - 1) & 1);
+                            if (ok) {
+                                bar_expect(q_full, tiles * Shape::kQTile + a.tx_extra);
+                                for (int t = 0; t < tiles; t++)
+                                    for (int c = 0; c < Shape::kChunks; c++)
+                                        tma_3d(base + t * Shape::kQTile + c * Shape::kQChunk, &q_map, q_full, c * 64, it.head,
+                                               it.q0 + it.row0 + t * kRows);
+                            }
+                            for (int u = 0; u < 2 * n && ok; u++) {
+                                const int s = (i + u) % kStages, round = (i + u) / kStages, j = u / 2;
+                                if (round > 0 && !(ok = bar_wait(empty + 8 * s, (round - 1) & 1))) break;
+                                bar_expect(full + 8 * s, Shape::kTile);
+                                for (int c = 0; c < Shape::kChunks; c++)
+                                    tma_3d(ring + s * Shape::kTile + c * Shape::kChunk, u % 2 ? &v_map : &k_map, full + 8 * s, c * 64, kv,
+                                           it.k0 + j * kKeys);
+                                // from here on the tile's barrier is in the phase that the look-over waits for
+                                if (u % 2 && j >= masked_from) bar_arrive(v_sent + 8 * ((g + j - masked_from) % kMarks));
+                            }
+                        }
+                        ok = __all_sync(~0u, ok);
+                        queries++;
+                        i += 2 * n;
+                        g += max(0, n - masked_from);
                     }
                 }
+                // asked for only now, when all of this item's copies are on their way: a CTA that asks earlier takes work
+                // that another could begin sooner
+                if (!ok) break;
+                if (lane == 0) ask_next(smem_u32(reply), asked);
+                if (!__all_sync(~0u, bar_wait(asked, answers++ & 1))) ok = false;
+                if (ok) block = next_block(smem_u32(reply));
+                __syncwarp();
             }
-            if (odd) special = 1;
-            fence_async_smem();
-            __syncwarp();
-            if (lane == 0) bar_arrive(v_seen + 8 * (j - masked_from));
+        } else if (warp == 11) {
+            // ---- values that some row must not see
+            PromptItem it;
+            int i = 0, g = 0;
+            for (int n_item = 0; ok && take(n_item, it); n_item++) {
+                const int n = max(it.key_tiles<kKeys>(0), it.key_tiles<kKeys>(1));
+                for (int j = it.masked_from<kKeys>(); j < n; j++, g++) {
+                    const int iv = i + 2 * j + 1;
+                    if (!__all_sync(~0u, bar_wait(v_sent + 8 * (g % kMarks), g / kMarks & 1) && bar_wait(full + 8 * (iv % kStages), iv / kStages & 1))) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t tile = ring + iv % kStages * Shape::kTile;
+                    const int there = min(it.klen - j * kKeys, kKeys);  // keys of the tile that exist (one at least)
+                    // a piece of 16 bytes is of key u / 8 (the swizzle moves pieces inside a row of 128 bytes only);
+                    // exponents of all ones carry into the sign bit
+                    constexpr uint32_t kExp = Half<T>::kExp, kOne = kExp == 0x7C007C00u ? 0x04000400u : 0x00800080u;
+                    uint32_t odd = 0;
+#pragma unroll 1
+                    for (int c = 0; c < Shape::kChunks; c++) {
+                        const uint32_t chunk = tile + c * Shape::kChunk;
+#pragma unroll 8
+                        for (int u = lane; u < there * 8; u += 32) {
+                            uint32_t x[4];
+                            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                         : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
+                                         : "r"(chunk + u * 16));
+#pragma unroll
+                            for (int w = 0; w < 4; w++) odd |= (x[w] & kExp) + kOne;
+                        }
+                        for (int u = there * 8 + lane; u < kKeys * 8; u += 32)
+                            asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(chunk + u * 16), "r"(0) : "memory");
+                    }
+                    if (odd & 0x80008000u) special[n_item % 4] = n_item + 1;  // (at most two items ahead of a softmax warp)
+                    fence_async_smem();
+                    __syncwarp();
+                    if (lane == 0) bar_arrive(v_seen + 8 * (g % kMarks));
+                }
+                i += 2 * n;
+            }
+        } else {
+            // ---- MMAs of query tile t (a warp each: neither waits for the other's softmax)
+            const int t = warp - 8;
+            constexpr uint32_t kScores = kAccF32 | Half<T>::kA | Half<T>::kB | mma_shape(kRows, kKeys);
+            constexpr uint32_t kValues = kAccF32 | Half<T>::kA | Half<T>::kB | kBMajorMN | mma_shape(kRows, D);
+            const uint32_t tS = tmem + Shape::kS + t * kKeys, tP = tmem + Shape::kP + t * (kKeys / 2), tO = tmem + Shape::kO + t * D;
+            PromptItem it;
+            int i = 0, g = 0, queries = 0, steps = 0, outputs = 0, turns = 0;
+            for (int n_item = 0; ok && take(n_item, it); n_item++) {
+                const int n0 = it.key_tiles<kKeys>(0), n1 = it.key_tiles<kKeys>(1), n = max(n0, n1), nt = t ? n1 : n0,
+                          masked_from = it.masked_from<kKeys>();
+                if (n == 0) continue;
+                if (elect_one()) {
+                    auto arrived = [&](int k) { return bar_wait(full + 8 * ((i + k) % kStages), (i + k) / kStages & 1); };
+                    // S = Q K^T for the item's key tile j, when the scores before it have been taken
+                    auto scores = [&](int j) {
+                        const int k = 2 * j, x0 = steps + j;
+                        if (!arrived(k) || (j < nt && x0 > 0 && !bar_wait(s_read + 8 * t, (x0 - 1) & 1))) return false;
+                        if (j < nt) {
+                            tc_fence_after();
+                            const uint32_t qa = base + t * Shape::kQTile, ka = ring + (i + k) % kStages * Shape::kTile;
+#pragma unroll
+                            for (int x = 0; x < D / 16; x++)
+                                mma_f16(tS, operand_desc(qa + x / 4 * Shape::kQChunk + x % 4 * 32, 16, 1024),
+                                        operand_desc(ka + x / 4 * Shape::kChunk + x % 4 * 32, 16, 1024), kScores, x > 0);
+                            mma_commit(s_full + 8 * t);
+                        }
+                        if (j + 1 == max(nt, 1)) mma_commit(q_empty + 8 * t);
+                        mma_commit(empty + 8 * ((i + k) % kStages));  // (without MMAs before it, this arrives at once)
+                        return true;
+                    };
+                    // The second tile begins when the first is through most of its first exponentials: side by side the
+                    // two look for maxima together and then share the exponential unit, and leave that state only
+                    // slowly (128 keys of 64 channels: 3600 cycles in step, 2800 out of step).
+                    ok = bar_wait(q_full, queries & 1) && (t == 0 || n0 == 0 || bar_wait(turn, turns & 1)) && scores(0);
+                    for (int j = 0; j < n && ok; j++) {
+                        if (j + 1 < n && !(ok = scores(j + 1))) break;
+                        const int k = 2 * j + 1, gv = g + j - masked_from;
+                        if (!(ok = arrived(k))) break;
+                        if (j < nt) {
+                            if (j >= masked_from && !(ok = bar_wait(v_seen + 8 * (gv % kMarks), gv / kMarks & 1))) break;
+                            // the item before has taken its output away
+                            if (j == 0 && outputs > 0 && !(ok = bar_wait(o_empty + 8 * t, (outputs - 1) & 1))) break;
+                            if (!(ok = bar_wait(p_full + 8 * t, (steps + j) & 1))) break;
+                            tc_fence_after();
+                            const uint32_t va = ring + (i + k) % kStages * Shape::kTile;
+#pragma unroll
+                            for (int x = 0; x < kKeys / 16; x++)
+                                mma_f16_ta(tO, tP + x * 8, operand_desc(va + x * 2048, Shape::kChunk, 1024), kValues, j > 0 || x > 0);
+                            mma_commit(p_read + 8 * t);
+                            if (j + 1 == nt) mma_commit(o_full + 8 * t);
+                        }
+                        mma_commit(empty + 8 * ((i + k) % kStages));
+                    }
+                }
+                ok = __all_sync(~0u, ok);
+                i += 2 * n;
+                g += max(0, n - masked_from);
+                queries++;
+                steps += nt;
+                outputs += nt > 0;
+                turns += n0 > 0;
+            }
         }
     } else {
         // ---- softmax: a row a thread
-        const int t = warp / 4, nt = t ? n1 : n0, row = row0 + tid;
-        const uint32_t lanes = static_cast<uint32_t>(warp % 4 * 32) << 16, st = tmem + t * kRows + lanes, ot = tmem + 2 * kRows + t * 128 + lanes;
-        const int first = row0 + t * kRows;
-        const int sees = row + offset;  // the last key of this row
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        const int t = warp / 4;
+        const uint32_t lanes = static_cast<uint32_t>(warp % 4 * 32) << 16, st = tmem + Shape::kS + t * kKeys + lanes,
+                       pt = tmem + Shape::kP + t * (kKeys / 2) + lanes, ot = tmem + Shape::kO + t * D + lanes;
         const float c = a.scale_log2;
-        float m = -INFINITY, l = 0.0f;  // m in units of the raw scores
-        for (int j = 0; j < nt; j++) {
-            if (!__all_sync(~0u, bar_wait(s_full + 8 * t, j & 1))) {
-                ok = false;
-                break;
-            }
-            tc_fence_after();
-            uint32_t s[kRows];
+        PromptItem it;
+        int steps = 0, outputs = 0;
+        for (int n_item = 0; ok && take(n_item, it); n_item++) {
+            const int nt = it.key_tiles<kKeys>(t), first = it.row0 + t * kRows, row = it.row0 + tid;
+            const int sees = row + it.offset();  // the last key of this row
+            float m = -INFINITY, l = 0.0f;       // m in units of the raw scores
+            for (int j = 0; j < nt; j++) {
+                if (!__all_sync(~0u, bar_wait(s_full + 8 * t, (steps + j) & 1))) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                uint32_t s[kKeys];
 #pragma unroll
-            for (int x = 0; x < kRows; x += 32) tmem_ld32(st + x, s + x);
-            tmem_wait_ld<kRows>(s);
-            if (j * kRows + kRows - 1 > first + offset) {
-                const int last = sees - j * kRows;
+                for (int x = 0; x < kKeys; x += 32) tmem_ld32(st + x, s + x);
+                tmem_wait_ld<kKeys>(s);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) bar_arrive(s_read + 8 * t);
+                if (j * kKeys + kKeys - 1 > first + it.offset()) {
+                    const int last = sees - j * kKeys;
 #pragma unroll
-                for (int x = 0; x < kRows; x++)
-                    if (x > last) s[x] = 0xFF800000u;
-            }
-            float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    for (int x = 0; x < kKeys; x++)
+                        if (x > last) s[x] = 0xFF800000u;
+                }
+                float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int x = 0; x < kRows; x++) top[x % 4] = fmaxf(top[x % 4], __uint_as_float(s[x]));
-            const float n_m = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-            const bool raise = n_m * c > m * c + kLazyLog2;
-            if (__any_sync(~0u, raise)) {
-                const float f = raise ? exp2_fast((m - n_m) * c) : 1.0f;
-                if (raise) m = n_m;
-                l *= f;
-                if (j > 0) {
-                    // O holds everything up to the last tile: its MMAs came before the scores that were waited for
+                for (int x = 0; x < kKeys; x += 2) top[x / 2 % 4] = max3(top[x / 2 % 4], __uint_as_float(s[x]), __uint_as_float(s[x + 1]));
+                const float n_m = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+                const bool raise = n_m * c > m * c + kLazyLog2;
+                bool read = steps + j == 0;  // the last weights, by their MMAs
+                if (__any_sync(~0u, raise)) {
+                    const float f = raise ? exp2_fast((m - n_m) * c) : 1.0f;
+                    if (raise) m = n_m;
+                    l *= f;
+                    if (j > 0) {
+                        if (!__all_sync(~0u, bar_wait(p_read + 8 * t, (steps + j - 1) & 1))) {
+                            ok = false;
+                            break;
+                        }
+                        read = true;
+                        tc_fence_after();
 #pragma unroll 1
-                    for (int x = 0; x < D; x += 32) {
-                        uint32_t o[32];
-                        tmem_ld32(ot + x, o);
-                        tmem_wait_ld<32>(o);
+                        for (int x = 0; x < D; x += 32) {
+                            uint32_t o[32];
+                            tmem_ld32(ot + x, o);
+                            tmem_wait_ld<32>(o);
 #pragma unroll
-                        for (int y = 0; y < 32; y++) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
-                        tmem_st32(ot + x, o);
+                            for (int y = 0; y < 32; y++) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
+                            tmem_st32(ot + x, o);
+                        }
                     }
                 }
-            }
-            const float less = (m == -INFINITY ? 0.0f : -m * c) + kBias;
-            float sum[2] = {0.0f, 0.0f};
+                const float less = (m == -INFINITY ? 0.0f : -m * c) + kBias;
+                const uint64_t c2 = pair(c, c), less2 = pair(less, less);
+                uint64_t sum[2] = {pair(0.0f, 0.0f), pair(0.0f, 0.0f)};
+                uint32_t p[kKeys / 2];
 #pragma unroll
-            for (int x = 0; x < kRows; x += 64) {
-                uint32_t p[32];
-#pragma unroll
-                for (int y = 0; y < 32; y++) {
-                    const float e0 = exp2_fast(fmaf(__uint_as_float(s[x + 2 * y]), c, less));
-                    const float e1 = exp2_fast(fmaf(__uint_as_float(s[x + 2 * y + 1]), c, less));
-                    sum[0] += e0;
-                    sum[1] += e1;
+                for (int y = 0; y < kKeys / 2; y++) {
+                    if (y == kKeys * 3 / 8 && t == 0 && j == 0 && lane == 0) bar_arrive(turn);
+                    const float2 v = halves(fma2(pair(s[2 * y], s[2 * y + 1]), c2, less2));
+                    const float e0 = exp2_fast(v.x), e1 = exp2_fast(v.y);
+                    sum[y % 2] = add2(sum[y % 2], pair(e0, e1));
                     p[y] = Half<T>::pack(e0, e1);
                 }
-                tmem_st32(st + x / 2, p);
-            }
-            l += sum[0] + sum[1];
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) bar_arrive(p_full + 8 * t);
-        }
-        if (ok && nt > 0) {
-            ok = __all_sync(~0u, bar_wait(o_full + 8 * t, 0));
-            tc_fence_after();
-        }
-        if (ok && first < qlen) {
-            const float by = l == 0.0f ? 0.0f : 1.0f / l;
-            T *out = static_cast<T *>(a.out) + (static_cast<int64_t>(q0) + row) * a.out_token + head * a.out_head;
-#pragma unroll 1
-            for (int x = 0; x < D; x += 32) {
-                uint32_t o[32];
-                if (nt > 0) {
-                    tmem_ld32(ot + x, o);
-                    tmem_wait_ld<32>(o);
+                if (!read && !__all_sync(~0u, bar_wait(p_read + 8 * t, (steps + j - 1) & 1))) {
+                    ok = false;
+                    break;
                 }
-                if (row < qlen) {
+                tc_fence_after();
+                if (kKeys >= 64) tmem_st32(pt, p);
+                if (kKeys == 96) tmem_st16(pt + 32, p + 32);
+                if (kKeys == 128) tmem_st32(pt + 32, p + 32);
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) bar_arrive(p_full + 8 * t);
+                const float2 both = halves(add2(sum[0], sum[1]));
+                l += both.x + both.y;
+            }
+            if (ok && nt > 0) {
+                ok = __all_sync(~0u, bar_wait(o_full + 8 * t, outputs & 1));
+                tc_fence_after();
+            }
+            if (!ok) break;
+            if (first < it.qlen) {
+                const float by = l == 0.0f ? 0.0f : 1.0f / l;
+                T *out = static_cast<T *>(a.out) + (static_cast<int64_t>(it.q0) + row) * a.out_token + it.head * a.out_head;
+#pragma unroll 1
+                for (int x = 0; x < D; x += 32) {
+                    uint32_t o[32];
+                    if (nt > 0) {
+                        tmem_ld32(ot + x, o);
+                        tmem_wait_ld<32>(o);
+                    }
+                    if (row < it.qlen) {
 #pragma unroll
-                    for (int y = 0; y < 32; y += 8) {
-                        uint32_t h[4];
+                        for (int y = 0; y < 32; y += 8) {
+                            uint32_t h[4];
 #pragma unroll
-                        for (int z = 0; z < 4; z++)
-                            h[z] = l == 0.0f ? 0u : Half<T>::pack(__uint_as_float(o[y + 2 * z]) * by, __uint_as_float(o[y + 2 * z + 1]) * by);
-                        *reinterpret_cast<uint4 *>(out + x + y) = make_uint4(h[0], h[1], h[2], h[3]);
+                            for (int z = 0; z < 4; z++)
+                                h[z] = l == 0.0f ? 0u : Half<T>::pack(__uint_as_float(o[y + 2 * z]) * by, __uint_as_float(o[y + 2 * z + 1]) * by);
+                            *reinterpret_cast<uint4 *>(out + x + y) = make_uint4(h[0], h[1], h[2], h[3]);
+                        }
                     }
                 }
             }
+            if (nt > 0) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) bar_arrive(o_empty + 8 * t);
+                // (this tile's values have all been looked over before its output was complete)
+                if (*static_cast<volatile int *>(&special[n_item % 4]) == n_item + 1)
+                    for (int r = it.row0 + warp * 32; r < min(it.row0 + warp * 32 + 32, it.qlen); r++)
+                        row_by_row<T, D>(a, it.head, static_cast<int64_t>(it.q0) + r, it.k0, min(max(r + it.offset() + 1, 0), it.klen));
+            }
+            steps += nt;
+            outputs += nt > 0;
         }
     }
     if (!ok) failed = 1;
@@ -395,9 +586,6 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     if (failed) {
         if (tid == 0) set_status(a.status, ENTRO_E_TIMEOUT);
         drain();
-    } else if (special) {
-        for (int r = row0 + warp; r < min(row0 + 256, qlen); r += kPromptThreads / 32)
-            row_by_row<T, D>(a, head, static_cast<int64_t>(q0) + r, k0, min(max(r + offset + 1, 0), klen));
     }
     tc_fence_before();
     __syncthreads();
@@ -413,11 +601,11 @@ static const void *pick_prompt(int dim, size_t *smem) {
                        : reinterpret_cast<const void *>(prompt_kernel<T, 128>);
 }
 
-// [tokens][heads][dim] for TMA boxes of 128 tokens of 64 channels of a head
-static int rows_map(CUtensorMap *map, int type, const void *base, int64_t tokens, int heads, int dim, int64_t token, int64_t head) {
+// [tokens][heads][dim] for TMA boxes of `rows` tokens of 64 channels of a head
+static int rows_map(CUtensorMap *map, int type, const void *base, int64_t tokens, int heads, int dim, int64_t token, int64_t head, int rows) {
     const uint64_t dims[3] = {static_cast<uint64_t>(dim), static_cast<uint64_t>(heads), static_cast<uint64_t>(tokens)};
     const uint64_t strides[2] = {static_cast<uint64_t>(heads > 1 ? head : dim) * 2, static_cast<uint64_t>(tokens > 1 ? token : dim) * 2};
-    const uint32_t box[3] = {64, 1, kRows};
+    const uint32_t box[3] = {64, 1, static_cast<uint32_t>(rows)};
     return encode_map(map, type == ENTRO_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, base, dims, strides, box);
 }
 
@@ -462,12 +650,13 @@ extern "C" int entro_attention_prompt(int32_t type, int32_t head_dim, const void
     if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
     size_t smem;
     const void *fn = type == ENTRO_BF16 ? pick_prompt<__nv_bfloat16>(head_dim, &smem) : pick_prompt<__half>(head_dim, &smem);
+    const int keys_of = head_dim == 64 ? PromptShape<64>::kKeys : head_dim == 96 ? PromptShape<96>::kKeys : PromptShape<128>::kKeys;
     int r = allow_smem(fn, dev);
     CUtensorMap q_map, k_map, v_map;
-    if (r == ENTRO_OK) r = rows_map(&q_map, type, d_q, tokens, heads, head_dim, q_token, q_head);
+    if (r == ENTRO_OK) r = rows_map(&q_map, type, d_q, tokens, heads, head_dim, q_token, q_head, kRows);
     // (without keys nothing is copied; the maps only have to be valid)
-    if (r == ENTRO_OK) r = keys ? rows_map(&k_map, type, d_k, keys, kv_heads, head_dim, k_token, k_head) : (k_map = q_map, ENTRO_OK);
-    if (r == ENTRO_OK) r = keys ? rows_map(&v_map, type, d_v, keys, kv_heads, head_dim, v_token, v_head) : (v_map = q_map, ENTRO_OK);
+    if (r == ENTRO_OK) r = keys ? rows_map(&k_map, type, d_k, keys, kv_heads, head_dim, k_token, k_head, keys_of) : (k_map = q_map, ENTRO_OK);
+    if (r == ENTRO_OK) r = keys ? rows_map(&v_map, type, d_v, keys, kv_heads, head_dim, v_token, v_head, keys_of) : (v_map = q_map, ENTRO_OK);
     if (r != ENTRO_OK) return r;
     void *args[] = {&q_map, &k_map, &v_map, &a};
     e = launch_ex(fn, dim3(static_cast<unsigned>(blocks)), kPromptThreads, smem, static_cast<cudaStream_t>(stream), 1, false, args);

@@ -33,7 +33,7 @@ __device__ __forceinline__ void wait_for_prior_grid() { asm volatile("griddepcon
 
 // After a wait gave up: nothing is issued any more, and copies in flight get ten
 // milliseconds to land before the CTA's shared memory is given back.
-static __device__ __noinline__ void drain() {
+__device__ __forceinline__ void drain() {
     const long long t0 = clock64();
     while (clock64() - t0 < (1LL << 24)) {
     }
@@ -69,7 +69,7 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
         : "memory");
     return ok != 0;
 }
-static __device__ __noinline__ bool bar_wait_slow(uint32_t bar, uint32_t parity) {
+__device__ __forceinline__ bool bar_wait_slow(uint32_t bar, uint32_t parity) {
     const long long t0 = clock64();
     while (!bar_try(bar, parity))
         if (clock64() - t0 > kWaitCycles) return false;
