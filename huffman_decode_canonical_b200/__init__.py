@@ -279,20 +279,22 @@ class DeviceTensor:
         quantized to 8 bits each with its scale, and multiplied in integers (`matmul_i8`)."""
         if not isinstance(x, QuantTokens) and (x.dim() != 2 or x.shape[1] != self.cols):
             raise ValueError("x must be a [tokens, cols] tensor")
-        with _on(self.device, stream) as s:
-            codes = self.empty_codes()
-            _check(_lib.entro_decode_codes(self._h, _dptr(codes), _dptr(status), s), "entro_decode_codes")
-            if self.bits == 8 and self.cols % 16 == 0:
-                w = codes[:self.n].view(self.rows, self.cols)
-            else:
-                pitch = _pitch(self.cols)
-                w = torch.empty((self.rows, pitch), dtype=torch.uint8, device=self.device)
-                _check(_lib.entro_unpack_codes(_dptr(codes), self.bits, self.rows, self.cols, _dptr(w), pitch, s),
-                       "entro_unpack_codes")
-                w = w[:, :self.cols]
-            xq = x if isinstance(x, QuantTokens) else quantize_tokens(x, stream=stream)
-            return matmul_i8(xq, w, self.info["scale"], self.info["zero"], out=out, out_dtype=out_dtype, status=status,
-                             stream=stream)
+        if stream is not None or self.device.index != _current_device():
+            with _on(self.device, stream):
+                return self.matmul(x, out, out_dtype, status)
+        s = _current_stream(self.device.index)
+        codes = self.empty_codes()
+        _check(_lib.entro_decode_codes(self._h, _dptr(codes), _dptr(status), s), "entro_decode_codes")
+        if self.bits == 8 and self.cols % 16 == 0:
+            w = codes[:self.n].view(self.rows, self.cols)
+        else:
+            pitch = _pitch(self.cols)
+            w = torch.empty((self.rows, pitch), dtype=torch.uint8, device=self.device)
+            _check(_lib.entro_unpack_codes(_dptr(codes), self.bits, self.rows, self.cols, _dptr(w), pitch, s),
+                   "entro_unpack_codes")
+            w = w[:, :self.cols]
+        xq = x if isinstance(x, QuantTokens) else quantize_tokens(x)
+        return matmul_i8(xq, w, self.info["scale"], self.info["zero"], out=out, out_dtype=out_dtype, status=status)
 
     def close(self):
         if getattr(self, "_h", None) and _lib is not None:
@@ -370,39 +372,37 @@ F32, BF16, F16, U8, S8 = range(5)
 _TYPES = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16, torch.uint8: U8, torch.int8: S8}
 
 
+# The current device and its current stream's handle, without the objects that the public calls make of them.
+_current_device = torch._C._cuda_getDevice
+_current_stream = torch._C._cuda_getCurrentRawStream
+
+
 class _on:
-    """The tensors' device as the current one, and new buffers from the pool of the stream that is launched on."""
+    """The tensors' device as the current one, and `stream` as its current stream: new buffers then come from the pool of
+    the stream that is launched on."""
 
     def __init__(self, device: torch.device, stream: Optional[torch.cuda.Stream]):
-        self.guards = []
-        if stream is not None:
-            if stream.device != device:
-                raise ValueError("the stream belongs to another device than the tensors")
-            self.guards.append(torch.cuda.stream(stream))
-        elif device.index != torch.cuda.current_device():
-            self.guards.append(torch.cuda.device(device))
-        self.device = device
+        if stream is not None and stream.device != device:
+            raise ValueError("the stream belongs to another device than the tensors")
+        self.guard = torch.cuda.device(device) if stream is None else torch.cuda.stream(stream)
 
-    def __enter__(self) -> int:
-        for g in self.guards:
-            g.__enter__()
-        return torch.cuda.current_stream(self.device).cuda_stream
+    def __enter__(self):
+        self.guard.__enter__()
 
     def __exit__(self, *e):
-        for g in reversed(self.guards):
-            g.__exit__(*e)
+        self.guard.__exit__(*e)
 
 
-def _inputs(device: torch.device, **tensors):
+def _check_inputs(index: int, tensors, names):
     """Refuses what the kernels must not be given: tensors of other devices, or ones that ask for gradients."""
-    if device.type != "cuda":
+    if index < 0:
         raise ValueError("expected CUDA tensors")
-    for name, t in tensors.items():
-        if t is None:
-            continue
-        if t.device != device:
-            raise ValueError(f"{name} is on {t.device}, not on {device}")
-        if t.requires_grad and torch.is_grad_enabled():
+    grad = torch.is_grad_enabled()
+    for t in tensors:
+        if t is not None and (t.get_device() != index or (grad and t.requires_grad)):
+            name = names[[u is t for u in tensors].index(True)]
+            if t.get_device() != index:
+                raise ValueError(f"{name} is on {t.device}, not on cuda:{index}")
             raise ValueError(f"{name} requires a gradient: this call has none (use torch.no_grad())")
 
 
@@ -422,16 +422,19 @@ def quantize_tokens(x: torch.Tensor, stream: Optional[torch.cuda.Stream] = None)
     """bf16 or fp16 [tokens, cols] (any row stride) to codes 127 x / max|x| of each token, with scale max|x| / 127."""
     if x.dtype not in (torch.bfloat16, torch.float16) or x.dim() != 2 or x.shape[1] < 1 or x.stride(1) != 1:
         raise ValueError("x must be a bf16 or fp16 [tokens, cols] tensor with adjacent columns")
-    _inputs(x.device, x=x)
+    index = x.get_device()
+    _check_inputs(index, (x,), ("x",))
+    if stream is not None or index != _current_device():
+        with _on(x.device, stream):
+            return quantize_tokens(x)
     tokens, cols = x.shape
-    pitch = _pitch(cols)
-    with _on(x.device, stream) as s:
-        codes = torch.empty((tokens, pitch), dtype=torch.int8, device=x.device)
-        scale = torch.empty(tokens, dtype=torch.float32, device=x.device)
-        total = torch.empty(tokens, dtype=torch.int32, device=x.device)
-        _check(_lib.entro_quantize_tokens(x.data_ptr(), _TYPES[x.dtype], tokens, cols, x.stride(0) if tokens > 1 else pitch,
-                                          codes.data_ptr(), pitch, scale.data_ptr(), total.data_ptr(), s),
-               "entro_quantize_tokens")
+    pitch, device = (cols + 15) // 16 * 16, x.device
+    codes = torch.empty((tokens, pitch), dtype=torch.int8, device=device)
+    scale = torch.empty(tokens, dtype=torch.float32, device=device)
+    total = torch.empty(tokens, dtype=torch.int32, device=device)
+    _check(_lib.entro_quantize_tokens(x.data_ptr(), _TYPES[x.dtype], tokens, cols, x.stride(0) if tokens > 1 else pitch,
+                                      codes.data_ptr(), pitch, scale.data_ptr(), total.data_ptr(), _current_stream(index)),
+           "entro_quantize_tokens")
     return QuantTokens(codes if pitch == cols else codes[:, :cols], scale, total)
 
 
@@ -442,63 +445,70 @@ def matmul_i8(x: QuantTokens, w: torch.Tensor, w_scale: Union[float, torch.Tenso
 
     w uint8 or int8 [rows, cols], adjacent columns, rows a multiple of 16 bytes apart; w_scale a number or fp32 [rows];
     w_zero a whole number, int32 [rows] or None (0).  out: fp32, bf16 or fp16 [tokens, rows] with adjacent columns."""
-    q = x.codes
+    q, scale, total = x
     if w.dtype not in (torch.uint8, torch.int8) or w.dim() != 2 or w.shape[1] < 1 or w.stride(1) != 1:
         raise ValueError("w must be a uint8 or int8 [rows, cols] tensor with adjacent columns")
     rows, cols = w.shape
-    tokens = q.shape[0] if q.dim() == 2 else -1
-    if q.dtype != torch.int8 or q.dim() != 2 or q.shape[1] != cols or q.stride(1) != 1:
+    if q.dtype is not torch.int8 or q.dim() != 2 or q.shape[1] != cols or q.stride(1) != 1:
         raise ValueError("x.codes must be an int8 [tokens, cols] tensor with adjacent columns")
-    for t, dtype, name in ((x.scale, torch.float32, "x.scale"), (x.sum, torch.int32, "x.sum")):
-        if t.dtype != dtype or t.shape != (tokens,) or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous {dtype} [tokens] tensor")
-    ws, wz = torch.is_tensor(w_scale), torch.is_tensor(w_zero)
-    if ws and (w_scale.dtype != torch.float32 or w_scale.shape != (rows,) or not w_scale.is_contiguous()):
-        raise ValueError("w_scale must be a number or a contiguous fp32 [rows] tensor")
-    if wz and (w_zero.dtype != torch.int32 or w_zero.shape != (rows,) or not w_zero.is_contiguous()):
-        raise ValueError("w_zero must be a whole number or a contiguous int32 [rows] tensor")
-    if not wz and w_zero is not None and not -2 ** 31 <= w_zero < 2 ** 31:
+    tokens = q.shape[0]
+    _vector(scale, "x.scale", torch.float32, tokens, "[tokens]")
+    _vector(total, "x.sum", torch.int32, tokens, "[tokens]")
+    ws, wz = isinstance(w_scale, torch.Tensor), isinstance(w_zero, torch.Tensor)
+    if ws:
+        _vector(w_scale, "w_scale", torch.float32, rows, "[rows]")
+    if wz:
+        _vector(w_zero, "w_zero", torch.int32, rows, "[rows]")
+    elif w_zero is None:
+        w_zero = 0
+    elif not -2 ** 31 <= w_zero < 2 ** 31:
         raise ValueError("w_zero must fit 32 bits")
-    _inputs(w.device, w=w, codes=q, scale=x.scale, sum=x.sum, w_scale=w_scale if ws else None, w_zero=w_zero if wz else None,
-            out=out, status=status)
+    index = w.get_device()
+    _check_inputs(index, (w, q, scale, total, w_scale if ws else None, w_zero if wz else None, out, status),
+                  ("w", "x.codes", "x.scale", "x.sum", "w_scale", "w_zero", "out", "status"))
     # a single row's stride says nothing
     ldq, ldw = (q.stride(0) if tokens > 1 else _pitch(cols)), (w.stride(0) if rows > 1 else _pitch(cols))
-    if ldq % 16 or ldw % 16 or q.data_ptr() % 16 or w.data_ptr() % 16:
+    qp, wp = q.data_ptr(), w.data_ptr()
+    if (ldq | ldw | qp | wp) & 15:
         raise ValueError("x.codes and w must begin on 16 bytes, their rows a multiple of 16 bytes apart")
-    with _on(w.device, stream) as s:
-        if out is None:
-            out = torch.empty((tokens, rows), dtype=out_dtype, device=w.device)
-        elif out.shape != (tokens, rows) or (rows > 1 and out.stride(1) != 1) or (tokens > 1 and out.stride(0) < rows):
+    if stream is not None or index != _current_device():
+        with _on(w.device, stream):
+            return matmul_i8(x, w, w_scale, w_zero, out, out_dtype, status)
+    if out is None:
+        out = torch.empty((tokens, rows), dtype=out_dtype, device=w.device)
+        ldy = rows
+    else:
+        if out.shape != (tokens, rows) or (rows > 1 and out.stride(1) != 1) or (tokens > 1 and out.stride(0) < rows):
             raise ValueError("out must be a [tokens, rows] tensor with adjacent columns")
-        if out.dtype not in (torch.float32, torch.bfloat16, torch.float16):
-            raise ValueError("out must be fp32, bf16 or fp16")
-        _check(_lib.entro_matmul_i8(q.data_ptr(), ldq, x.scale.data_ptr(), x.sum.data_ptr(), tokens, w.data_ptr(), _TYPES[w.dtype],
-                                    ldw, rows, cols, w_scale.data_ptr() if ws else None, 0.0 if ws else float(w_scale),
-                                    w_zero.data_ptr() if wz else None, 0 if wz or w_zero is None else int(w_zero),
-                                    out.data_ptr(), _TYPES[out.dtype], out.stride(0) if tokens > 1 else rows,
-                                    _dptr(status), s), "entro_matmul_i8")
+        ldy = out.stride(0) if tokens > 1 else rows
+    if out.dtype not in (torch.float32, torch.bfloat16, torch.float16):
+        raise ValueError("out must be fp32, bf16 or fp16")
+    _check(_lib.entro_matmul_i8(qp, ldq, scale.data_ptr(), total.data_ptr(), tokens, wp, _TYPES[w.dtype], ldw, rows, cols,
+                                w_scale.data_ptr() if ws else None, 0.0 if ws else float(w_scale), w_zero.data_ptr() if wz else None,
+                                0 if wz else int(w_zero), out.data_ptr(), _TYPES[out.dtype], ldy,
+                                None if status is None else status.data_ptr(), _current_stream(index)), "entro_matmul_i8")
     return out
 
 
-def _rows(t: torch.Tensor, name: str, dtype: torch.dtype, heads: int, dim: int) -> torch.Tensor:
-    """A [tokens, heads, dim] tensor that the kernels can read in 16-byte pieces."""
-    if t.dtype != dtype or t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
+def _vector(t: torch.Tensor, name: str, dtype: torch.dtype, n: int, what: str):
+    if t.dtype is not dtype or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} {what} tensor")
+
+
+def _rows(t: torch.Tensor, name: str, dtype: torch.dtype, heads: int, dim: int):
+    """Token and head stride of a [tokens, heads, dim] tensor that the kernels can read in 16-byte pieces (those of a
+    single token or head say nothing and count as 0)."""
+    shape = t.shape
+    if t.dtype is not dtype or len(shape) != 3 or shape[1] != heads or shape[2] != dim:
         raise ValueError(f"{name} must be a {dtype} [tokens, {heads}, {dim}] tensor")
-    s = t.stride()
-    if s[2] != 1 or (t.shape[0] > 1 and s[0] % 8) or (heads > 1 and s[1] % 8) or t.data_ptr() % 16:
+    token, head, channel = t.stride()
+    if shape[0] <= 1:
+        token = 0
+    if heads <= 1:
+        head = 0
+    if channel != 1 or (token | head) & 7 or t.data_ptr() & 15:
         raise ValueError(f"{name} must have adjacent channels, strides that are multiples of 8 and begin on 16 bytes")
-    return t
-
-
-def _strides(t: torch.Tensor):
-    """Token and head stride; those of a single token or head say nothing."""
-    s = t.stride()
-    return (s[0] if t.shape[0] > 1 else 0), (s[1] if t.shape[1] > 1 else 0)
-
-
-def _index(t: torch.Tensor, name: str, shape: tuple):
-    if t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous int32 {list(shape)} tensor")
+    return token, head
 
 
 def attention_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor,
@@ -517,36 +527,39 @@ def attention_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqle
         raise ValueError("head_dim must be 64, 96 or 128")
     if kv < 1 or heads < 1 or heads % kv:
         raise ValueError("q's heads must be a multiple of k's")
-    _rows(q, "q", q.dtype, heads, dim)
-    _rows(k, "k", q.dtype, kv, dim)
-    _rows(v, "v", q.dtype, kv, dim)
+    dtype = q.dtype
+    qs, ks, vs = _rows(q, "q", dtype, heads, dim), _rows(k, "k", dtype, kv, dim), _rows(v, "v", dtype, kv, dim)
     if v.shape[0] != keys:
         raise ValueError("k and v must have the same number of tokens")
-    for t, name in ((q, "q"), (k, "k"), (v, "v")):
-        if (t.shape[0] > 1 and t.stride(0) == 0) or (t.shape[1] > 1 and t.stride(1) == 0):
-            raise ValueError(f"{name} must not be expanded")
+    if (tokens > 1 and qs[0] == 0) or (heads > 1 and qs[1] == 0) or (keys > 1 and 0 in (ks[0], vs[0])) or (kv > 1 and 0 in (ks[1], vs[1])):
+        raise ValueError("q, k and v must not be expanded")
     batch = cu_seqlens.shape[0] - 1 if cu_seqlens.dim() == 1 else -1
     if batch < 0:
         raise ValueError("cu_seqlens must be an int32 [batch + 1] tensor")
-    _index(cu_seqlens, "cu_seqlens", (batch + 1,))
+    _vector(cu_seqlens, "cu_seqlens", torch.int32, batch + 1, "[batch + 1]")
     if cu_keys is not None:
-        _index(cu_keys, "cu_keys", (batch + 1,))
+        _vector(cu_keys, "cu_keys", torch.int32, batch + 1, "[batch + 1]")
     elif keys != tokens:
         raise ValueError("without cu_keys, k and v must have q's tokens")
     if out is not None:
-        _rows(out, "out", q.dtype, heads, dim)
+        os_ = _rows(out, "out", dtype, heads, dim)
         if out.shape[0] != tokens:
             raise ValueError("out must have q's shape")
     scale = dim ** -0.5 if scale is None else float(scale)
     if not 0.0 < scale < 3e38:
         raise ValueError("scale must be above 0 and finite")
-    _inputs(q.device, q=q, k=k, v=v, cu_seqlens=cu_seqlens, cu_keys=cu_keys, out=out, status=status)
-    with _on(q.device, stream) as s:
-        out = torch.empty((tokens, heads, dim), dtype=q.dtype, device=q.device) if out is None else out
-        _check(_lib.entro_attention_prompt(_TYPES[q.dtype], dim, q.data_ptr(), *_strides(q), heads, tokens, k.data_ptr(), *_strides(k),
-                                           v.data_ptr(), *_strides(v), kv, keys, cu_seqlens.data_ptr(),
-                                           cu_keys.data_ptr() if cu_keys is not None else None, batch, scale, out.data_ptr(),
-                                           *_strides(out), _dptr(status), s), "entro_attention_prompt")
+    index = q.get_device()
+    _check_inputs(index, (q, k, v, cu_seqlens, cu_keys, out, status), ("q", "k", "v", "cu_seqlens", "cu_keys", "out", "status"))
+    if stream is not None or index != _current_device():
+        with _on(q.device, stream):
+            return attention_prompt(q, k, v, cu_seqlens, cu_keys, scale, out, status)
+    if out is None:
+        out = torch.empty((tokens, heads, dim), dtype=dtype, device=q.device)
+        os_ = (heads * dim, dim)
+    _check(_lib.entro_attention_prompt(_TYPES[dtype], dim, q.data_ptr(), *qs, heads, tokens, k.data_ptr(), *ks, v.data_ptr(), *vs, kv,
+                                       keys, cu_seqlens.data_ptr(), None if cu_keys is None else cu_keys.data_ptr(), batch, scale,
+                                       out.data_ptr(), *os_, None if status is None else status.data_ptr(), _current_stream(index)),
+           "entro_attention_prompt")
     return out
 
 
@@ -577,7 +590,9 @@ class KVCache:
             if t.dtype != want or t.shape != shape or not t.is_contiguous() or t.data_ptr() % 16:
                 raise ValueError(f"{name} must be a contiguous {want} {list(shape)} tensor that begins on 16 bytes")
         self.device = k_codes.device
-        _inputs(self.device, k_codes=k_codes, v_codes=v_codes, k_scale=k_scale, v_scale=v_scale, k_tail=k_tail, v_tail=v_tail)
+        self._index = k_codes.get_device()
+        _check_inputs(self._index, (k_codes, v_codes, k_scale, v_scale, k_tail, v_tail),
+                      ("k_codes", "v_codes", "k_scale", "v_scale", "k_tail", "v_tail"))
         self.k_codes, self.v_codes, self.k_scale, self.v_scale, self.k_tail, self.v_tail = k_codes, v_codes, k_scale, v_scale, k_tail, v_tail
         self.pages, self.kv_heads, self.page_tokens, self.head_dim, self.slots, self.dtype = pages, kv, page, dim, slots, dtype
         self._c = _KVCache(k_codes.data_ptr(), v_codes.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), k_tail.data_ptr(),
@@ -594,54 +609,68 @@ class KVCache:
         tails = [torch.empty((slots, kv_heads, page_tokens, head_dim), dtype=dtype, device=device) for _ in range(2)]
         return cls(*codes, *scales, *tails)
 
-    def _tables(self, page_table: torch.Tensor, slots: Optional[torch.Tensor]) -> int:
-        if page_table.dtype != torch.int32 or page_table.dim() != 2 or (page_table.shape[1] > 1 and page_table.stride(1) != 1):
-            raise ValueError("page_table must be an int32 [batch, width] tensor with adjacent columns")
-        batch = page_table.shape[0]
+    def _tables(self, page_table: torch.Tensor, slots: Optional[torch.Tensor]):
+        """(batch, width, row stride) of a page table"""
+        if page_table.dtype is not torch.int32 or page_table.dim() != 2:
+            raise ValueError("page_table must be an int32 [batch, width] tensor")
+        batch, width = page_table.shape
+        stride, one = page_table.stride()
+        if batch <= 1:
+            stride = width
+        if (width > 1 and one != 1) or stride < width:
+            raise ValueError("page_table must have adjacent columns")
         if slots is not None:
-            _index(slots, "slots", (batch,))
+            _vector(slots, "slots", torch.int32, batch, "[batch]")
         elif batch > self.slots:
             raise ValueError("more sequences than tail slots")
-        return batch
+        return batch, width, stride
 
     def append(self, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor, page_table: torch.Tensor, lens: torch.Tensor,
                slots: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
                stream: Optional[torch.cuda.Stream] = None) -> None:
         """Packed new tokens k, v [tokens, kv_heads, head_dim] to their sequences; cu_seqlens int32 [batch + 1] says where
         each sequence's begin, lens counts them already.  No page or slot may be written for two sequences."""
-        _rows(k, "k", self.dtype, self.kv_heads, self.head_dim)
-        _rows(v, "v", self.dtype, self.kv_heads, self.head_dim)
-        if k.shape[0] != v.shape[0]:
+        ks, vs = _rows(k, "k", self.dtype, self.kv_heads, self.head_dim), _rows(v, "v", self.dtype, self.kv_heads, self.head_dim)
+        tokens = k.shape[0]
+        if tokens != v.shape[0]:
             raise ValueError("k and v must have the same number of tokens")
-        batch = self._tables(page_table, slots)
-        _index(cu_seqlens, "cu_seqlens", (batch + 1,))
-        _index(lens, "lens", (batch,))
-        _inputs(self.device, k=k, v=v, cu_seqlens=cu_seqlens, page_table=page_table, lens=lens, slots=slots, status=status)
-        with _on(self.device, stream) as s:
-            _check(_lib.entro_kv_append(self._ref, k.data_ptr(), *_strides(k), v.data_ptr(), *_strides(v), k.shape[0],
-                                        cu_seqlens.data_ptr(), page_table.data_ptr(), page_table.stride(0) if batch > 1 else page_table.shape[1],
-                                        page_table.shape[1], lens.data_ptr(), slots.data_ptr() if slots is not None else None, batch,
-                                        _dptr(status), s), "entro_kv_append")
+        batch, width, stride = self._tables(page_table, slots)
+        _vector(cu_seqlens, "cu_seqlens", torch.int32, batch + 1, "[batch + 1]")
+        _vector(lens, "lens", torch.int32, batch, "[batch]")
+        index = self._index
+        _check_inputs(index, (k, v, cu_seqlens, page_table, lens, slots, status),
+                      ("k", "v", "cu_seqlens", "page_table", "lens", "slots", "status"))
+        if stream is not None or index != _current_device():
+            with _on(self.device, stream):
+                return self.append(k, v, cu_seqlens, page_table, lens, slots, status)
+        _check(_lib.entro_kv_append(self._ref, k.data_ptr(), *ks, v.data_ptr(), *vs, tokens, cu_seqlens.data_ptr(), page_table.data_ptr(),
+                                    stride, width, lens.data_ptr(), None if slots is None else slots.data_ptr(), batch,
+                                    None if status is None else status.data_ptr(), _current_stream(index)), "entro_kv_append")
 
     def read(self, page_table: torch.Tensor, cu_seqlens: torch.Tensor, tokens: int, slots: Optional[torch.Tensor] = None,
              out: Optional[tuple] = None, status: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None):
         """(k, v) [tokens, kv_heads, head_dim]: all tokens of the sequences, packed; sequence b holds
         cu_seqlens[b + 1] - cu_seqlens[b] of them."""
-        batch = self._tables(page_table, slots)
-        _index(cu_seqlens, "cu_seqlens", (batch + 1,))
+        batch, width, stride = self._tables(page_table, slots)
+        _vector(cu_seqlens, "cu_seqlens", torch.int32, batch + 1, "[batch + 1]")
+        heads, dim = self.kv_heads, self.head_dim
+        k, v = (None, None) if out is None else out
         if out is not None:
-            for t, name in zip(out, ("k", "v")):
-                _rows(t, name, self.dtype, self.kv_heads, self.head_dim)
-                if t.shape[0] != tokens:
-                    raise ValueError(f"{name} must have {tokens} tokens")
-        _inputs(self.device, cu_seqlens=cu_seqlens, page_table=page_table, slots=slots, status=status,
-                k=out[0] if out is not None else None, v=out[1] if out is not None else None)
-        with _on(self.device, stream) as s:
-            k, v = out if out is not None else (torch.empty((tokens, self.kv_heads, self.head_dim), dtype=self.dtype, device=self.device)
-                                                for _ in range(2))
-            _check(_lib.entro_kv_read(self._ref, k.data_ptr(), *_strides(k), v.data_ptr(), *_strides(v), tokens, cu_seqlens.data_ptr(),
-                                      page_table.data_ptr(), page_table.stride(0) if batch > 1 else page_table.shape[1], page_table.shape[1],
-                                      slots.data_ptr() if slots is not None else None, batch, _dptr(status), s), "entro_kv_read")
+            ks, vs = _rows(k, "k", self.dtype, heads, dim), _rows(v, "v", self.dtype, heads, dim)
+            if k.shape[0] != tokens or v.shape[0] != tokens:
+                raise ValueError(f"out must have {tokens} tokens")
+        index = self._index
+        _check_inputs(index, (cu_seqlens, page_table, slots, k, v, status), ("cu_seqlens", "page_table", "slots", "k", "v", "status"))
+        if stream is not None or index != _current_device():
+            with _on(self.device, stream):
+                return self.read(page_table, cu_seqlens, tokens, slots, out, status)
+        if out is None:
+            k = torch.empty((tokens, heads, dim), dtype=self.dtype, device=self.device)
+            v = torch.empty((tokens, heads, dim), dtype=self.dtype, device=self.device)
+            ks = vs = (heads * dim, dim)
+        _check(_lib.entro_kv_read(self._ref, k.data_ptr(), *ks, v.data_ptr(), *vs, tokens, cu_seqlens.data_ptr(), page_table.data_ptr(),
+                                  stride, width, None if slots is None else slots.data_ptr(), batch,
+                                  None if status is None else status.data_ptr(), _current_stream(index)), "entro_kv_read")
         return k, v
 
     def attend(self, q: torch.Tensor, page_table: torch.Tensor, lens: torch.Tensor, slots: Optional[torch.Tensor] = None,
@@ -649,34 +678,39 @@ class KVCache:
                stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
         """Attention of one token of each sequence, q [batch, heads, head_dim] (heads a multiple of kv_heads), over its
         cached tokens; scale: 1 / sqrt(head_dim) by default.  A sequence without tokens gets zeros."""
-        heads = q.shape[1] if q.dim() == 3 else 0
-        _rows(q, "q", self.dtype, heads, self.head_dim)
+        heads, dim = q.shape[1] if q.dim() == 3 else 0, self.head_dim
+        qs = _rows(q, "q", self.dtype, heads, dim)
         if heads < 1 or heads % self.kv_heads:
             raise ValueError("q's heads must be a multiple of the cache's")
-        batch = self._tables(page_table, slots)
+        batch, width, stride = self._tables(page_table, slots)
         if q.shape[0] != batch:
             raise ValueError("q must have a token for each sequence")
-        _index(lens, "lens", (batch,))
+        _vector(lens, "lens", torch.int32, batch, "[batch]")
         if out is not None:
-            _rows(out, "out", self.dtype, heads, self.head_dim)
+            os_ = _rows(out, "out", self.dtype, heads, dim)
             if out.shape[0] != batch:
                 raise ValueError("out must have q's shape")
-        scale = self.head_dim ** -0.5 if scale is None else float(scale)
+        scale = dim ** -0.5 if scale is None else float(scale)
         if not 0.0 < scale < 3e38:
             raise ValueError("scale must be above 0 and finite")
-        _inputs(self.device, q=q, page_table=page_table, lens=lens, slots=slots, out=out, status=status)
-        with _on(self.device, stream) as s:
-            if self._work_bytes is None:
-                n = ctypes.c_uint64()
-                _check(_lib.entro_kv_attend_workspace(self._ref, ctypes.byref(n)), "entro_kv_attend_workspace")
-                self._work_bytes = n.value
-            # a workspace of the call's own, from the pool of the stream it runs on: calls never share one
-            work = torch.empty(self._work_bytes, dtype=torch.uint8, device=self.device)
-            out = torch.empty((batch, heads, self.head_dim), dtype=self.dtype, device=self.device) if out is None else out
-            _check(_lib.entro_kv_attend(self._ref, q.data_ptr(), *_strides(q), heads, page_table.data_ptr(),
-                                        page_table.stride(0) if batch > 1 else page_table.shape[1], page_table.shape[1], lens.data_ptr(),
-                                        slots.data_ptr() if slots is not None else None, batch, scale, out.data_ptr(), *_strides(out),
-                                        work.data_ptr(), self._work_bytes, _dptr(status), s), "entro_kv_attend")
+        index = self._index
+        _check_inputs(index, (q, page_table, lens, slots, out, status), ("q", "page_table", "lens", "slots", "out", "status"))
+        if stream is not None or index != _current_device():
+            with _on(self.device, stream):
+                return self.attend(q, page_table, lens, slots, scale, out, status)
+        if self._work_bytes is None:
+            n = ctypes.c_uint64()
+            _check(_lib.entro_kv_attend_workspace(self._ref, ctypes.byref(n)), "entro_kv_attend_workspace")
+            self._work_bytes = n.value
+        # a workspace of the call's own, from the pool of the stream it runs on: calls never share one
+        work = torch.empty(self._work_bytes, dtype=torch.uint8, device=self.device)
+        if out is None:
+            out = torch.empty((batch, heads, dim), dtype=self.dtype, device=self.device)
+            os_ = (heads * dim, dim)
+        _check(_lib.entro_kv_attend(self._ref, q.data_ptr(), *qs, heads, page_table.data_ptr(), stride, width, lens.data_ptr(),
+                                    None if slots is None else slots.data_ptr(), batch, scale, out.data_ptr(), *os_, work.data_ptr(),
+                                    self._work_bytes, None if status is None else status.data_ptr(), _current_stream(index)),
+               "entro_kv_attend")
         return out
 
 

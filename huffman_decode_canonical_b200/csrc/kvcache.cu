@@ -232,6 +232,7 @@ struct AttendArgs {
     int32_t *status;
     int batch, group, chunks;  // query heads of a key head; groups of 8 of them
     int table_width, ctas;
+    bool join_early;  // the join may begin, and find its place, while the pieces are computed
     float scale_log2;
 };
 
@@ -260,20 +261,17 @@ struct Shares {
     }
 };
 
-// Sums over the batch: all tiles of one head, and those of the sequences before
-// the one that `pick` selects.  pick(tiles before, tiles of this sequence) is
-// true for at most one sequence.
+// All tiles of one head over the batch, and the sequence that `pick` chooses with the tiles before it: pick(b, tiles
+// before b, tiles of b, all tiles) is true for one sequence at most.  A batch of up to a CTA's threads is read once.
 template <typename Pick>
 __device__ __forceinline__ int64_t scan_batch(const AttendArgs &a, int &seq, int64_t &before, Pick pick) {
     __shared__ int64_t warp_sum[kAttendThreads / 32], picked_before;
     __shared__ int picked;
     const int tid = threadIdx.x, lane = tid % 32;
-    int64_t total = 0;
-    __syncthreads();
+    int64_t total = 0, at = 0, tiles = 0;
     if (tid == 0) picked = -1;
-    for (int b0 = 0; b0 < a.batch; b0 += kAttendThreads) {
-        const int b = b0 + tid;
-        const int64_t tiles = b < a.batch ? (static_cast<int64_t>(clean_len(a, b, false)) + kTile - 1) / kTile : 0;
+    auto chunk = [&](int b) {  // at: tiles before sequence b; total: those of all chunks so far
+        tiles = b < a.batch ? (static_cast<int64_t>(clean_len(a, b, false)) + kTile - 1) / kTile : 0;
         int64_t sum = tiles;
         for (int o = 1; o < 32; o *= 2) {
             const int64_t up = __shfl_up_sync(~0u, sum, o);
@@ -281,20 +279,34 @@ __device__ __forceinline__ int64_t scan_batch(const AttendArgs &a, int &seq, int
         }
         if (lane == 31) warp_sum[tid / 32] = sum;
         __syncthreads();
-        int64_t at = total + sum - tiles;
+        at = total + sum - tiles;
         for (int w = 0; w < kAttendThreads / 32; w++) {
             if (w < tid / 32) at += warp_sum[w];
             total += warp_sum[w];
         }
-        if (b < a.batch && pick(b, at, tiles)) {
+        __syncthreads();
+    };
+    for (int b0 = 0; b0 < a.batch; b0 += kAttendThreads) chunk(b0 + tid);
+    const int64_t all = total;
+    auto offer = [&](int b) {
+        if (b < a.batch && pick(b, at, tiles, all)) {
             picked = b;
             picked_before = at;
         }
-        __syncthreads();
+    };
+    if (a.batch <= kAttendThreads) {
+        offer(tid);
+    } else {
+        total = 0;
+        for (int b0 = 0; b0 < a.batch; b0 += kAttendThreads) {
+            chunk(b0 + tid);
+            offer(b0 + tid);
+        }
     }
+    __syncthreads();
     seq = picked;
     before = picked_before;
-    return total;
+    return all;
 }
 
 // Four codes to two pairs of 16-bit floats, exactly: 1024 + (code + 128) has the
@@ -319,6 +331,41 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// Asynchronous copies to shared memory, in groups a thread.
+__device__ __forceinline__ void copy_async16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_async4(uint32_t dst, const void *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void close_group() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void wait_groups() {  // all but the last N groups have landed
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// A step's 16 tokens of codes in shared memory: rows of D bytes, their 16-byte pieces moved so that the eight lanes of
+// a phase meet eight different ones -- keys: lanes read strips of D / 4 bytes of rows gid; values: strips of D / 8
+// bytes of rows 2 tig.  (96: no move needed for the keys, two lanes a bank for the values.)
+template <int D>
+struct StepLayout {
+    static constexpr int kCodes = 16 * D, kBytes = 2 * kCodes + 16;  // keys, values, their two scales
+    static __device__ __forceinline__ uint32_t key(int row, int byte) {
+        return D == 128 ? row * 128 + (byte ^ ((row & 1) * 16)) : row * D + byte;
+    }
+    static __device__ __forceinline__ uint32_t value(int row, int byte) {
+        if (D == 96) return row * D + byte;
+        const int at = row * D + byte, line = D == 128 ? row / 2 : row / 2;  // (rows 2 tig: a line of 128 bytes each, or two)
+        return at ^ ((line & 3) * 32);
+    }
+};
+template <int N>
+__device__ __forceinline__ void load_shared(uint32_t *r, uint32_t at) {
+    if (N == 16) asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at));
+    else if (N == 8) asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(at));
+    else asm volatile("ld.shared.u32 %0, [%1];" : "=r"(r[0]) : "r"(at));
+}
+
 // N bytes (8, 12, 16, 24 or 32) from an address aligned to the largest power of two in N
 template <int N>
 __device__ __forceinline__ void load_bytes(uint32_t *r, const void *p) {
@@ -412,23 +459,36 @@ struct Running {
 // where the (sequence, head) changes; a piece that covers all of its sequence and
 // head is finished here, others leave (m, l, o) behind for the join.  Bound by
 // reading the codes (2 D bytes of a token and key head).
+constexpr int kSteps = 3;  // a warp's steps in flight: with 16 warps on an SM three times what the memory's latency needs
+
+template <int D>
+constexpr int attend_smem() {
+    const int steps = 4 * kSteps * StepLayout<D>::kBytes, join = 4 * kHeads * (D + 4) * 4;
+    return steps > join ? steps : join;
+}
+
 template <typename T, int D>
 __global__ void __launch_bounds__(kAttendThreads, 4) attend_kernel(const AttendArgs a) {
+    using Layout = StepLayout<D>;
     constexpr int kK = D / 4, kV = D / 8;  // bytes of a token's codes that a thread reads: keys (2 tokens), values (4)
+    constexpr int kKLoad = kK % 16 == 0 ? 16 : 8, kVLoad = kV % 16 == 0 ? 16 : kV % 8 == 0 ? 8 : 4;
+    extern __shared__ __align__(16) uint8_t smem[];  // the warps' steps, then their outputs
     __shared__ float sm_m[4][kHeads], sm_l[4][kHeads];
-    __shared__ __align__(16) float sm_o[4][kHeads][D + 4];  // read and written in pairs
-    wait_for_prior_grid();
+    float(*sm_o)[kHeads][D + 4] = reinterpret_cast<float(*)[kHeads][D + 4]>(smem);
+    if (a.join_early) dependents_may_launch();
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, gid = lane / 4, tig = lane % 4;
+    const uint32_t steps = smem_u32(smem) + warp * kSteps * Layout::kBytes;
     const int P = 1 << a.c.log_page, cols = a.c.kv * a.chunks;
     int seq;
     int64_t before;
-    // first pass for the total, second for the sequence of this share's first tile
-    const int64_t total = scan_batch(a, seq, before, [](int, int64_t, int64_t) { return false; }) * cols;
+    const int64_t total = scan_batch(a, seq, before, [&](int, int64_t at, int64_t tiles, int64_t all) {
+        const int64_t first = Shares(all * cols, a.ctas).begin(blockIdx.x);
+        return first >= at * cols && first < (at + tiles) * cols;
+    }) * cols;
     const Shares shares(total, a.ctas);
     int64_t at = shares.begin(blockIdx.x);
     const int64_t stop = shares.begin(blockIdx.x + 1);
     if (at >= stop) return;
-    scan_batch(a, seq, before, [&](int, int64_t b4, int64_t tiles) { return at >= b4 * cols && at < (b4 + tiles) * cols; });
     int64_t seq_at = before * cols;
     while (at < stop) {
         // the piece: tiles [t0, t1) of column (key head, chunk of query heads) of the sequence
@@ -445,6 +505,40 @@ __global__ void __launch_bounds__(kAttendThreads, 4) attend_kernel(const AttendA
         const int heads = min(kHeads, a.group - col % a.chunks * kHeads);
         const int full = len >> a.c.log_page << a.c.log_page;  // tokens in coded blocks
         const int32_t *pages = a.table + seq * a.table_stride;
+
+        // Steps of 16 tokens, kSteps - 1 of them on their way.  A step that is not of coded blocks (the tail's, past the
+        // end, on a page that does not exist) copies nothing; bit x of `coded` says of the step in place x whether it did.
+        uint32_t coded = 0;
+        int place = 0;  // of the next step to be sent
+        auto page_of = [&](int tile) {
+            const int tok = tile * kTile + warp * 16;
+            return tile < t1 && tok < full ? __ldg(pages + (tok >> a.c.log_page)) : -1;
+        };
+        int page = page_of(t0);
+        auto send = [&](int tile) {
+            const int tok = tile * kTile + warp * 16, p = page;
+            page = page_of(tile + 1);
+            coded &= ~(1u << place);
+            if (tile < t1 && tok < full) {
+                if (p >= 0 && p < a.c.pages) {
+                    const int64_t block = static_cast<int64_t>(p) * a.c.kv + h, from = (block * P + (tok & (P - 1))) * D;
+                    const uint32_t to = steps + place * Layout::kBytes;
+#pragma unroll
+                    for (int i = 0; i < D / 32; i++) {
+                        const int piece = i * 32 + lane, row = piece / (D / 16), byte = piece % (D / 16) * 16;
+                        copy_async16(to + Layout::key(row, byte), a.c.codes[0] + from + piece * 16);
+                        copy_async16(to + Layout::kCodes + Layout::value(row, byte), a.c.codes[1] + from + piece * 16);
+                    }
+                    if (lane < 2) copy_async4(to + 2 * Layout::kCodes + lane * 4, a.c.scale[lane] + block);
+                    coded |= 1u << place;
+                } else {
+                    set_status(a.status, ENTRO_E_INVAL);
+                }
+            }
+            close_group();
+            place = place + 1 == kSteps ? 0 : place + 1;
+        };
+        for (int i = 0; i < kSteps - 1; i++) send(t0 + i);
 
         // Q as the second operand: head gid, channels tig D / 4 + 4 s + 0 .. 3 in step s
         uint32_t q[D / 16][2];
@@ -467,46 +561,28 @@ __global__ void __launch_bounds__(kAttendThreads, 4) attend_kernel(const AttendA
 
         Running<D> r;
         r.clear();
-        // 16 tokens a step; a thread's keys are tokens gid and gid + 8, its values tokens 2 tig, 2 tig + 1 and those + 8
-        uint32_t kr[2][kK / 4], vr[4][kV / 4];
-        float ks = 0.0f, vs = 0.0f, next_ks = 0.0f, next_vs = 0.0f;
-        const int8_t *next_k = nullptr, *next_v = nullptr;
-        // where step `tile`'s codes are (null: in the tail, past the end, or on no page)
-        auto locate = [&](int tile) {
-            const int tok = tile * kTile + warp * 16;
-            next_k = next_v = nullptr;
-            if (tile >= t1 || tok >= full) return;
-            const int page = __ldg(pages + (tok >> a.c.log_page));
-            if (page < 0 || page >= a.c.pages) {
-                set_status(a.status, ENTRO_E_INVAL);
-                return;
-            }
-            const int64_t block = static_cast<int64_t>(page) * a.c.kv + h, row = block * P + (tok & (P - 1));
-            next_k = a.c.codes[0] + (row + gid) * D + tig * kK;
-            next_v = a.c.codes[1] + (row + 2 * tig) * D + gid * kV;
-            next_ks = __ldg(a.c.scale[0] + block);
-            next_vs = __ldg(a.c.scale[1] + block);
-        };
-        auto load_k = [&]() {
-            if (next_k) {
-                load_bytes<kK>(kr[0], next_k);
-                load_bytes<kK>(kr[1], next_k + 8 * D);
-            }
-        };
-        auto load_v = [&]() {
-            if (next_v) {
-#pragma unroll
-                for (int j = 0; j < 4; j++) load_bytes<kV>(vr[j], next_v + (j / 2 * 8 + j % 2) * D);
-            }
-        };
-        locate(t0);
-        load_k();
-        load_v();
+        // a thread's keys are tokens gid and gid + 8, its values tokens 2 tig, 2 tig + 1 and those + 8
+        int here = 0;
         for (int tile = t0; tile < t1; tile++) {
             const int tok = tile * kTile + warp * 16;
-            const bool coded = next_k != nullptr;
-            ks = next_ks, vs = next_vs;
-            if (coded) {
+            send(tile + kSteps - 1);
+            wait_groups<kSteps - 1>();
+            __syncwarp();
+            if (coded >> here & 1) {
+                const uint32_t from = steps + here * Layout::kBytes;
+                uint32_t kr[2][kK / 4], vr[4][kV / 4];
+                float ks, vs;
+                asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(ks), "=f"(vs) : "r"(from + 2 * Layout::kCodes));
+#pragma unroll
+                for (int i = 0; i < kK; i += kKLoad) {
+                    load_shared<kKLoad>(kr[0] + i / 4, from + Layout::key(gid, tig * kK + i));
+                    load_shared<kKLoad>(kr[1] + i / 4, from + Layout::key(gid + 8, tig * kK + i));
+                }
+#pragma unroll
+                for (int i = 0; i < kV; i += kVLoad)
+#pragma unroll
+                    for (int j = 0; j < 4; j++)
+                        load_shared<kVLoad>(vr[j] + i / 4, from + Layout::kCodes + Layout::value(2 * tig + j / 2 * 8 + j % 2, gid * kV + i));
                 float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                 for (int s = 0; s < D / 16; s++) {
@@ -515,8 +591,6 @@ __global__ void __launch_bounds__(kAttendThreads, 4) attend_kernel(const AttendA
                                            sub2(__byte_perm(lo, 0x64646464u, 0x4342)), sub2(__byte_perm(hi, 0x64646464u, 0x4342))};
                     mma16816(c, f, q[s][0], q[s][1]);
                 }
-                locate(tile + 1);
-                load_k();  // in flight beside this step's softmax and values
                 const float f0 = qs[0] * ks, f1 = qs[1] * ks;
                 const float s[4] = {c[0] * f0, c[1] * f1, c[2] * f0, c[3] * f1};
                 uint32_t p0, p1;
@@ -537,7 +611,6 @@ __global__ void __launch_bounds__(kAttendThreads, 4) attend_kernel(const AttendA
                         o[0] += w[0] * vs, o[1] += w[1] * vs, o[2] += w[2] * vs, o[3] += w[3] * vs;
                     }
                 }
-                load_v();
             } else {
                 const int slot = a.slot_of ? a.slot_of[seq] : seq;
                 const bool slot_ok = slot >= 0 && slot < a.c.slots;
@@ -603,13 +676,14 @@ __global__ void __launch_bounds__(kAttendThreads, 4) attend_kernel(const AttendA
                         for (int j = 0; j < 4; j++) r.o[i][j] += w[j] * inverse;
                     }
                 }
-                locate(tile + 1);
-                load_k();
-                load_v();
             }
+            __syncwarp();  // the step's place is sent to again
+            here = here + 1 == kSteps ? 0 : here + 1;
         }
+        wait_groups<0>();
 
         // the four warps' parts meet in shared memory
+        __syncthreads();
 #pragma unroll
         for (int x = 4; x < 32; x *= 2) {
             r.l[0] += __shfl_xor_sync(~0u, r.l[0], x);
@@ -662,12 +736,11 @@ __global__ void __launch_bounds__(kAttendThreads, 4) attend_kernel(const AttendA
 // without tokens get zeros.
 template <typename T, int D>
 __global__ void __launch_bounds__(kAttendThreads) join_kernel(const AttendArgs a) {
-    wait_for_prior_grid();
     const int tid = threadIdx.x, cols = a.c.kv * a.chunks;
     const int seq = static_cast<int>(blockIdx.x / cols), col = static_cast<int>(blockIdx.x % cols);
     int got;
     int64_t before;
-    const int64_t total = scan_batch(a, got, before, [&](int b, int64_t, int64_t) { return b == seq; }) * cols;
+    const int64_t total = scan_batch(a, got, before, [&](int b, int64_t, int64_t, int64_t) { return b == seq; }) * cols;
     const int h = col / a.chunks, head0 = h * a.group + col % a.chunks * kHeads;
     const int heads = min(kHeads, a.group - col % a.chunks * kHeads);
     const int tiles = (clean_len(a, seq, true) + kTile - 1) / kTile;
@@ -677,8 +750,9 @@ __global__ void __launch_bounds__(kAttendThreads) join_kernel(const AttendArgs a
     if (tiles > 0) {
         first = shares.owner(t0);
         last = shares.owner(t0 + tiles - 1);
-        if (first == last) return;  // one CTA had it all
     }
+    wait_for_prior_grid();  // (the lengths above are no work of the grid before)
+    if (tiles > 0 && first == last) return;  // one CTA had it all
     for (int u = tid; u < heads * (D / 2); u += kAttendThreads) {
         const int head = u / (D / 2), d = u % (D / 2) * 2;
         float m = -INFINITY, l = 0.0f, o0 = 0.0f, o1 = 0.0f;
@@ -836,10 +910,18 @@ extern "C" int entro_kv_attend(const entro_kv_cache *cache, const void *d_q, int
     a.scale_log2 = scale * 1.4426950408889634f;
     const int64_t columns = static_cast<int64_t>(batch) * a.c.kv * a.chunks;
     if (columns > INT32_MAX) return ENTRO_E_LIMIT;
+    a.join_early = columns <= a.ctas / 4;  // a CTA on each SM at most, beside the four that are there
+    const size_t smem = cache->head_dim == 64 ? attend_smem<64>() : cache->head_dim == 96 ? attend_smem<96>() : attend_smem<128>();
+    const void *fn = ENTRO_BY_TYPE(cache, ENTRO_ATTEND);
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+    r = allow_smem(fn, dev);
+    if (r != ENTRO_OK) return r;
     void *args[] = {&a};
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    cudaError_t e = launch_ex(ENTRO_BY_TYPE(cache, ENTRO_ATTEND), dim3(a.ctas), kAttendThreads, 0, st, 1, false, args);
+    e = launch_ex(fn, dim3(a.ctas), kAttendThreads, smem, st, 1, false, args);
     if (e == cudaSuccess)
-        e = launch_ex(ENTRO_BY_TYPE(cache, ENTRO_JOIN), dim3(static_cast<unsigned>(columns)), kAttendThreads, 0, st, 1, columns <= a.ctas, args);
+        e = launch_ex(ENTRO_BY_TYPE(cache, ENTRO_JOIN), dim3(static_cast<unsigned>(columns)), kAttendThreads, 0, st, 1, a.join_early, args);
     return e == cudaSuccess ? ENTRO_OK : cuda_fail(e, "entro_kv_attend");
 }
