@@ -251,30 +251,30 @@ __device__ __forceinline__ int clean_len(const AttendArgs &a, int b, bool report
     return len < 0 ? 0 : static_cast<int>(most);
 }
 
-// All (sequence, head, tile)s in a row are cut into equal shares for the CTAs.
+// All (sequence, head, tile)s in a row (less than 2^31) are cut into equal shares for the CTAs.
 struct Shares {
-    int64_t each, more;  // the first `more` CTAs take one more than `each`
-    __device__ __forceinline__ Shares(int64_t total, int ctas) : each(total / ctas), more(total % ctas) {}
-    __device__ __forceinline__ int64_t begin(int64_t cta) const { return cta * each + min(cta, more); }
-    __device__ __forceinline__ int owner(int64_t tile) const {
-        return static_cast<int>(tile < more * (each + 1) ? tile / (each + 1) : more + (tile - more * (each + 1)) / each);
+    uint32_t each, more;  // the first `more` CTAs take one more than `each`
+    __device__ __forceinline__ Shares(uint32_t total, uint32_t ctas) : each(total / ctas), more(total % ctas) {}
+    __device__ __forceinline__ uint32_t begin(uint32_t cta) const { return cta * each + min(cta, more); }
+    __device__ __forceinline__ int owner(uint32_t tile) const {
+        return tile < more * (each + 1) ? tile / (each + 1) : more + (tile - more * (each + 1)) / each;
     }
 };
 
 // All tiles of one head over the batch, and the sequence that `pick` chooses with the tiles before it: pick(b, tiles
 // before b, tiles of b, all tiles) is true for one sequence at most.  A batch of up to a CTA's threads is read once.
 template <typename Pick>
-__device__ __forceinline__ int64_t scan_batch(const AttendArgs &a, int &seq, int64_t &before, Pick pick) {
-    __shared__ int64_t warp_sum[kAttendThreads / 32], picked_before;
+__device__ __forceinline__ uint32_t scan_batch(const AttendArgs &a, int &seq, uint32_t &before, Pick pick) {
+    __shared__ uint32_t warp_sum[kAttendThreads / 32], picked_before;
     __shared__ int picked;
     const int tid = threadIdx.x, lane = tid % 32;
-    int64_t total = 0, at = 0, tiles = 0;
+    uint32_t total = 0, at = 0, tiles = 0;
     if (tid == 0) picked = -1;
     auto chunk = [&](int b) {  // at: tiles before sequence b; total: those of all chunks so far
-        tiles = b < a.batch ? (static_cast<int64_t>(clean_len(a, b, false)) + kTile - 1) / kTile : 0;
-        int64_t sum = tiles;
+        tiles = b < a.batch ? (static_cast<uint32_t>(clean_len(a, b, false)) + kTile - 1) / kTile : 0;
+        uint32_t sum = tiles;
         for (int o = 1; o < 32; o *= 2) {
-            const int64_t up = __shfl_up_sync(~0u, sum, o);
+            const uint32_t up = __shfl_up_sync(~0u, sum, o);
             if (lane >= o) sum += up;
         }
         if (lane == 31) warp_sum[tid / 32] = sum;
@@ -287,7 +287,7 @@ __device__ __forceinline__ int64_t scan_batch(const AttendArgs &a, int &seq, int
         __syncthreads();
     };
     for (int b0 = 0; b0 < a.batch; b0 += kAttendThreads) chunk(b0 + tid);
-    const int64_t all = total;
+    const uint32_t all = total;
     auto offer = [&](int b) {
         if (b < a.batch && pick(b, at, tiles, all)) {
             picked = b;
@@ -480,27 +480,27 @@ __global__ void __launch_bounds__(kAttendThreads, 4) attend_kernel(const AttendA
     const uint32_t steps = smem_u32(smem) + warp * kSteps * Layout::kBytes;
     const int P = 1 << a.c.log_page, cols = a.c.kv * a.chunks;
     int seq;
-    int64_t before;
-    const int64_t total = scan_batch(a, seq, before, [&](int, int64_t at, int64_t tiles, int64_t all) {
-        const int64_t first = Shares(all * cols, a.ctas).begin(blockIdx.x);
+    uint32_t before;
+    const uint32_t total = scan_batch(a, seq, before, [&](int, uint32_t at, uint32_t tiles, uint32_t all) {
+        const uint32_t first = Shares(all * cols, a.ctas).begin(blockIdx.x);
         return first >= at * cols && first < (at + tiles) * cols;
     }) * cols;
     const Shares shares(total, a.ctas);
-    int64_t at = shares.begin(blockIdx.x);
-    const int64_t stop = shares.begin(blockIdx.x + 1);
+    uint32_t at = shares.begin(blockIdx.x);
+    const uint32_t stop = shares.begin(blockIdx.x + 1);
     if (at >= stop) return;
-    int64_t seq_at = before * cols;
+    uint32_t seq_at = before * cols;
     while (at < stop) {
         // the piece: tiles [t0, t1) of column (key head, chunk of query heads) of the sequence
         int len = clean_len(a, seq, true), tiles = (len + kTile - 1) / kTile;
-        while (at >= seq_at + static_cast<int64_t>(tiles) * cols) {  // (sequences without tokens have no tiles)
-            seq_at += static_cast<int64_t>(tiles) * cols;
+        while (at >= seq_at + static_cast<uint32_t>(tiles * cols)) {  // (sequences without tokens have no tiles)
+            seq_at += tiles * cols;
             seq++;
             len = clean_len(a, seq, true);
             tiles = (len + kTile - 1) / kTile;
         }
-        const int col = static_cast<int>((at - seq_at) / tiles), t0 = static_cast<int>((at - seq_at) % tiles);
-        const int t1 = static_cast<int>(min(static_cast<int64_t>(tiles), t0 + (stop - at)));
+        const int col = (at - seq_at) / static_cast<uint32_t>(tiles), t0 = (at - seq_at) % static_cast<uint32_t>(tiles);
+        const int t1 = min(static_cast<uint32_t>(tiles), t0 + (stop - at));
         const int h = col / a.chunks, head0 = h * a.group + col % a.chunks * kHeads;
         const int heads = min(kHeads, a.group - col % a.chunks * kHeads);
         const int full = len >> a.c.log_page << a.c.log_page;  // tokens in coded blocks
@@ -739,13 +739,13 @@ __global__ void __launch_bounds__(kAttendThreads) join_kernel(const AttendArgs a
     const int tid = threadIdx.x, cols = a.c.kv * a.chunks;
     const int seq = static_cast<int>(blockIdx.x / cols), col = static_cast<int>(blockIdx.x % cols);
     int got;
-    int64_t before;
-    const int64_t total = scan_batch(a, got, before, [&](int b, int64_t, int64_t, int64_t) { return b == seq; }) * cols;
+    uint32_t before;
+    const uint32_t total = scan_batch(a, got, before, [&](int b, uint32_t, uint32_t, uint32_t) { return b == seq; }) * cols;
     const int h = col / a.chunks, head0 = h * a.group + col % a.chunks * kHeads;
     const int heads = min(kHeads, a.group - col % a.chunks * kHeads);
     const int tiles = (clean_len(a, seq, true) + kTile - 1) / kTile;
     const Shares shares(total, a.ctas);
-    const int64_t t0 = before * cols + static_cast<int64_t>(col) * tiles;
+    const uint32_t t0 = before * cols + col * tiles;
     int first = 0, last = 0;
     if (tiles > 0) {
         first = shares.owner(t0);
@@ -753,21 +753,66 @@ __global__ void __launch_bounds__(kAttendThreads) join_kernel(const AttendArgs a
     }
     wait_for_prior_grid();  // (the lengths above are no work of the grid before)
     if (tiles > 0 && first == last) return;  // one CTA had it all
-    for (int u = tid; u < heads * (D / 2); u += kAttendThreads) {
-        const int head = u / (D / 2), d = u % (D / 2) * 2;
-        float m = -INFINITY, l = 0.0f, o0 = 0.0f, o1 = 0.0f;
-        for (int i = first; i <= last && tiles > 0; i++) {
-            const float *row = a.work + ((static_cast<int64_t>(i) * 2 + (i == first)) * kHeads + head) * (D + 2);
-            const float2 ml = *reinterpret_cast<const float2 *>(row), o = *reinterpret_cast<const float2 *>(row + 2 + d);
-            const float n = fmaxf(m, ml.x), fm = m == n ? 1.0f : ex2(m - n), f = ml.x == n ? 1.0f : ex2(ml.x - n);
-            l = l * fm + ml.y * f;
-            o0 = o0 * fm + o.x * f;
-            o1 = o1 * fm + o.y * f;
-            m = n;
+    // 64 pieces at a time: all their maxima and sums first (a piece's weight is 2^(its maximum - the largest)), then
+    // their outputs, with nothing between the loads
+    constexpr int kPieces = 64, kMine = kHeads * (D / 2) / kAttendThreads;
+    __shared__ float weight[kHeads][kPieces], rescale[kHeads], sum[kHeads], most[kHeads];
+    const int warp = tid / 32, lane = tid % 32;
+    auto row_of = [&](int i, int head) { return a.work + ((static_cast<int64_t>(i) * 2 + (i == first)) * kHeads + head) * (D + 2); };
+    float2 o[kMine];
+#pragma unroll
+    for (int u = 0; u < kMine; u++) o[u] = make_float2(0.0f, 0.0f);
+    if (tid < kHeads) most[tid] = -INFINITY, sum[tid] = 0.0f;
+    __syncthreads();
+    const int pieces = tiles > 0 ? last - first + 1 : 0;
+    for (int i0 = 0; i0 < pieces; i0 += kPieces) {
+        const int n = min(kPieces, pieces - i0);
+        for (int head = warp; head < heads; head += kAttendThreads / 32) {
+            float2 ml[2];
+#pragma unroll
+            for (int x = 0; x < 2; x++)
+                ml[x] = lane + 32 * x < n ? *reinterpret_cast<const float2 *>(row_of(first + i0 + lane + 32 * x, head)) : make_float2(-INFINITY, 0.0f);
+            float m = fmaxf(ml[0].x, ml[1].x);
+            for (int x = 16; x; x /= 2) m = fmaxf(m, __shfl_xor_sync(~0u, m, x));
+            const float was = most[head], now = fmaxf(was, m);
+            float l = 0.0f;
+#pragma unroll
+            for (int x = 0; x < 2; x++) {
+                const float w = ml[x].x == now ? 1.0f : ex2(ml[x].x - now);
+                weight[head][lane + 32 * x] = w;
+                l += w * ml[x].y;
+            }
+            for (int x = 16; x; x /= 2) l += __shfl_xor_sync(~0u, l, x);
+            __syncwarp();
+            if (lane == 0) {
+                const float f = was == now ? 1.0f : ex2(was - now);
+                rescale[head] = f;
+                sum[head] = sum[head] * f + l;
+                most[head] = now;
+            }
         }
-        const float by = l == 0.0f ? 0.0f : 1.0f / l;
+        __syncthreads();
+#pragma unroll
+        for (int u = 0; u < kMine; u++) {
+            const int unit = u * kAttendThreads + tid, head = unit / (D / 2), d = unit % (D / 2) * 2;
+            if (head >= heads) break;
+            o[u].x *= rescale[head], o[u].y *= rescale[head];
+#pragma unroll 8
+            for (int i = 0; i < n; i++) {
+                const float2 v = *reinterpret_cast<const float2 *>(row_of(first + i0 + i, head) + 2 + d);
+                o[u].x += weight[head][i] * v.x;
+                o[u].y += weight[head][i] * v.y;
+            }
+        }
+        __syncthreads();
+    }
+#pragma unroll
+    for (int u = 0; u < kMine; u++) {
+        const int unit = u * kAttendThreads + tid, head = unit / (D / 2), d = unit % (D / 2) * 2;
+        if (head >= heads) break;
+        const float by = sum[head] == 0.0f ? 0.0f : 1.0f / sum[head];
         T *out = static_cast<T *>(a.out) + seq * a.out_token + (head0 + head) * a.out_head + d;
-        *reinterpret_cast<uint32_t *>(out) = Half<T>::pack(o0 * by, o1 * by);
+        *reinterpret_cast<uint32_t *>(out) = Half<T>::pack(o[u].x * by, o[u].y * by);
     }
 }
 
@@ -909,7 +954,8 @@ extern "C" int entro_kv_attend(const entro_kv_cache *cache, const void *d_q, int
     a.batch = batch, a.group = heads / a.c.kv, a.chunks = (a.group + kHeads - 1) / kHeads;
     a.scale_log2 = scale * 1.4426950408889634f;
     const int64_t columns = static_cast<int64_t>(batch) * a.c.kv * a.chunks;
-    if (columns > INT32_MAX) return ENTRO_E_LIMIT;
+    // all tiles are counted in 32 bits
+    if (columns * (((static_cast<int64_t>(table_width) + 1) << a.c.log_page) / kTile + 1) > INT32_MAX) return ENTRO_E_LIMIT;
     a.join_early = columns <= a.ctas / 4;  // a CTA on each SM at most, beside the four that are there
     const size_t smem = cache->head_dim == 64 ? attend_smem<64>() : cache->head_dim == 96 ? attend_smem<96>() : attend_smem<128>();
     const void *fn = ENTRO_BY_TYPE(cache, ENTRO_ATTEND);

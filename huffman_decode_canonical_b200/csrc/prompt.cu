@@ -467,10 +467,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             const int sees = row + it.offset();  // the last key of this row
             float m = -INFINITY, l = 0.0f;       // m in units of the raw scores
             for (int j = 0; j < nt; j++) {
-                if (!__all_sync(~0u, bar_wait(s_full + 8 * t, (steps + j) & 1))) {
-                    ok = false;
-                    break;
-                }
+                ok = ok && bar_wait(s_full + 8 * t, (steps + j) & 1);  // (a wait that gave up is the last: no vote a step)
+                __syncwarp();
                 tc_fence_after();
                 uint32_t s[kKeys];
 #pragma unroll
@@ -496,10 +494,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                     if (raise) m = n_m;
                     l *= f;
                     if (j > 0) {
-                        if (!__all_sync(~0u, bar_wait(p_read + 8 * t, (steps + j - 1) & 1))) {
-                            ok = false;
-                            break;
-                        }
+                        ok = ok && bar_wait(p_read + 8 * t, (steps + j - 1) & 1);
+                        __syncwarp();
                         read = true;
                         tc_fence_after();
 #pragma unroll 1
@@ -515,21 +511,21 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                 }
                 const float less = (m == -INFINITY ? 0.0f : -m * c) + kBias;
                 const uint64_t c2 = pair(c, c), less2 = pair(less, less);
-                uint64_t sum[2] = {pair(0.0f, 0.0f), pair(0.0f, 0.0f)};
+                uint64_t sum[4] = {pair(0.0f, 0.0f), pair(0.0f, 0.0f), pair(0.0f, 0.0f), pair(0.0f, 0.0f)};
                 uint32_t p[kKeys / 2];
 #pragma unroll
                 for (int y = 0; y < kKeys / 2; y++) {
                     if (y == kKeys * 3 / 8 && t == 0 && j == 0 && lane == 0) bar_arrive(turn);
                     const float2 v = halves(fma2(pair(s[2 * y], s[2 * y + 1]), c2, less2));
                     const float e0 = exp2_fast(v.x), e1 = exp2_fast(v.y);
-                    sum[y % 2] = add2(sum[y % 2], pair(e0, e1));
+                    sum[y % 4] = add2(sum[y % 4], pair(e0, e1));
                     p[y] = Half<T>::pack(e0, e1);
                 }
-                if (!read && !__all_sync(~0u, bar_wait(p_read + 8 * t, (steps + j - 1) & 1))) {
-                    ok = false;
-                    break;
+                if (!read) {
+                    ok = ok && bar_wait(p_read + 8 * t, (steps + j - 1) & 1);
+                    __syncwarp();
+                    tc_fence_after();
                 }
-                tc_fence_after();
                 if (kKeys >= 64) tmem_st32(pt, p);
                 if (kKeys == 96) tmem_st16(pt + 32, p + 32);
                 if (kKeys == 128) tmem_st32(pt + 32, p + 32);
@@ -537,11 +533,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) bar_arrive(p_full + 8 * t);
-                const float2 both = halves(add2(sum[0], sum[1]));
+                const float2 both = halves(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])));
                 l += both.x + both.y;
             }
-            if (ok && nt > 0) {
-                ok = __all_sync(~0u, bar_wait(o_full + 8 * t, outputs & 1));
+            if (nt > 0) {
+                ok = __all_sync(~0u, ok && bar_wait(o_full + 8 * t, outputs & 1));
                 tc_fence_after();
             }
             if (!ok) break;
