@@ -154,11 +154,23 @@ struct ProductArgs {
     uint32_t idesc, tmem_cols, tx_extra;
 };
 
-__device__ __forceinline__ void store_out(void *y, int64_t at, float v, int type) {
-    if (type == OUT_F32) static_cast<float *>(y)[at] = v;
-    else if (type == OUT_BF16T) static_cast<__nv_bfloat16 *>(y)[at] = __float2bfloat16_rn(v);
-    else static_cast<__half *>(y)[at] = __float2half_rn(v);
-}
+template <int OUT>
+struct OutOf;
+template <>
+struct OutOf<OUT_F32> {
+    using Type = float;
+    static __device__ __forceinline__ float of(float v) { return v; }
+};
+template <>
+struct OutOf<OUT_BF16T> {
+    using Type = __nv_bfloat16;
+    static __device__ __forceinline__ __nv_bfloat16 of(float v) { return __float2bfloat16_rn(v); }
+};
+template <>
+struct OutOf<OUT_F16T> {
+    using Type = __half;
+    static __device__ __forceinline__ __half of(float v) { return __float2half_rn(v); }
+};
 
 // One channel's part of the epilogue.
 struct Channel {
@@ -172,11 +184,25 @@ struct Channel {
         wide = zero < -256 || zero > 256;
     }
     // acc - zero * sum: in the codes' range the difference is a sum of cols products of at most 127 * 511,
-    // below 2^31 for cols up to 32768; past that, or for other zero points, it is taken in 64 bits
-    __device__ __forceinline__ float value(int32_t acc, int32_t sum, float x_scale, bool in64) const {
+    // below 2^31 for cols up to 32768; past that, or for other zero points (in64), it is taken in 64 bits
+    template <bool in64>
+    __device__ __forceinline__ float value(int32_t acc, int32_t sum, float x_scale) const {
         const float v = in64 ? static_cast<float>(static_cast<long long>(acc) - static_cast<long long>(zero) * sum)
                              : static_cast<float>(acc - zero * sum);
         return v * (x_scale * scale);
+    }
+    // N tokens' outputs of this channel, the first at y, the next ones ldy further each; `left` of them exist
+    template <int OUT, int N, bool in64>
+    __device__ __forceinline__ void store(const uint32_t *acc, const float *xs, const int32_t *xz, typename OutOf<OUT>::Type *y,
+                                          int64_t ldy, int left) const {
+        if (left >= N) {
+#pragma unroll
+            for (int j = 0; j < N; j++, y += ldy) *y = OutOf<OUT>::of(value<in64>(static_cast<int32_t>(acc[j]), xz[j], xs[j]));
+        } else {
+#pragma unroll
+            for (int j = 0; j < N; j++, y += ldy)
+                if (j < left) *y = OutOf<OUT>::of(value<in64>(static_cast<int32_t>(acc[j]), xz[j], xs[j]));
+        }
     }
 };
 
@@ -196,6 +222,8 @@ __global__ void __launch_bounds__(192, 1) product_narrow_kernel(const __grid_con
     __shared__ __align__(8) uint64_t bars[2 * 16 + 1];
     __shared__ uint32_t tmem_base;
     __shared__ int failed;
+    __shared__ float xs[256];
+    __shared__ int32_t xz[256];
     const uint32_t base = (smem_u32(smem_raw) + 1023) & ~1023u;
     const int tid = threadIdx.x, warp = tid / 32;
     const int split = gridDim.x, part = blockIdx.x, tile = blockIdx.y;
@@ -252,6 +280,10 @@ __global__ void __launch_bounds__(192, 1) product_narrow_kernel(const __grid_con
             if (ok) mma_commit(done);
         }
     } else {
+        for (int t = tid; t < a.tokens; t += 128) {
+            xs[t] = a.x_scale[t];
+            xz[t] = a.x_sum[t];
+        }
         ok = bar_wait(done, 0);
         tc_fence_after();
     }
@@ -275,11 +307,10 @@ __global__ void __launch_bounds__(192, 1) product_narrow_kernel(const __grid_con
                 uint32_t r[16];
                 tmem_ld16(lanes + t0, r);
                 tmem_wait_ld<16>(r);
-#pragma unroll
-                for (int j = 0; j < 16; j++) {
-                    const int t = t0 + j;
-                    if (t < a.tokens && n < a.rows)
-                        store_out(a.y, t * a.ldy + n, ch.value(static_cast<int32_t>(r[j]), a.x_sum[t], a.x_scale[t], in64), OUT);
+                if (n < a.rows) {
+                    auto *y = static_cast<typename OutOf<OUT>::Type *>(a.y) + t0 * a.ldy + n;
+                    if (in64) ch.template store<OUT, 16, true>(r, xs + t0, xz + t0, y, a.ldy, a.tokens - t0);
+                    else ch.template store<OUT, 16, false>(r, xs + t0, xz + t0, y, a.ldy, a.tokens - t0);
                 }
             }
         }
@@ -287,15 +318,21 @@ __global__ void __launch_bounds__(192, 1) product_narrow_kernel(const __grid_con
         // [source CTA][token of the share][row]: every CTA's operands have been consumed behind the barrier
         cluster_sync();
         if (warp < 4) {
+            const uint32_t mine = base + (part * per * kTileRows + tid) * 4;
+            int owner = 0, in_share = 0;
+            uint32_t to = map_to(mine, 0);
             for (int t0 = 0; t0 < a.bn; t0 += 16) {
                 uint32_t r[16];
                 tmem_ld16(lanes + t0, r);
                 tmem_wait_ld<16>(r);
 #pragma unroll
                 for (int j = 0; j < 16; j++) {
-                    const int t = t0 + j, owner = t / per;
-                    const uint32_t to = map_to(base + ((part * per + t - owner * per) * kTileRows + tid) * 4, owner);
                     asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(to), "r"(r[j]) : "memory");
+                    to += kTileRows * 4;
+                    if (++in_share == per) {
+                        in_share = 0;
+                        to = map_to(mine, min(++owner, split - 1));
+                    }
                 }
             }
         }
@@ -304,13 +341,19 @@ __global__ void __launch_bounds__(192, 1) product_narrow_kernel(const __grid_con
             for (int j = 0; j < per; j++) {
                 const int t = part * per + j;
                 if (t >= a.tokens || t >= a.bn) break;
-                int32_t acc = 0;
-                for (int s = 0; s < split; s++) {
-                    int32_t v;
-                    asm volatile("ld.shared.s32 %0, [%1];" : "=r"(v) : "r"(base + ((s * per + j) * kTileRows + tid) * 4));
-                    acc += v;
+                int32_t v[8], acc = 0;
+#pragma unroll
+                for (int s = 0; s < 8; s++)
+                    if (s < split) asm volatile("ld.shared.s32 %0, [%1];" : "=r"(v[s]) : "r"(base + ((s * per + j) * kTileRows + tid) * 4));
+#pragma unroll
+                for (int s = 0; s < 8; s++)
+                    if (s < split) acc += v[s];
+                if (n < a.rows) {
+                    auto *y = static_cast<typename OutOf<OUT>::Type *>(a.y) + t * a.ldy + n;
+                    const uint32_t bits = static_cast<uint32_t>(acc);
+                    if (in64) ch.template store<OUT, 1, true>(&bits, xs + t, xz + t, y, a.ldy, 1);
+                    else ch.template store<OUT, 1, false>(&bits, xs + t, xz + t, y, a.ldy, 1);
                 }
-                if (n < a.rows) store_out(a.y, t * a.ldy + n, ch.value(acc, a.x_sum[t], a.x_scale[t], in64), OUT);
             }
         }
     }
@@ -450,12 +493,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1)
                 tmem_ld32(lanes + t0, r);
                 tmem_wait_ld<32>(r);
                 const int t = token * a.bn + t0;
-                if (ch_row < a.rows) {
-#pragma unroll
-                    for (int j = 0; j < 32; j++)
-                        if (t + j < a.tokens)
-                            store_out(a.y, (t + j) * a.ldy + ch_row,
-                                      ch.value(static_cast<int32_t>(r[j]), xz[acc][t0 + j], xs[acc][t0 + j], in64), OUT);
+                if (ch_row < a.rows && t < a.tokens) {
+                    auto *y = static_cast<typename OutOf<OUT>::Type *>(a.y) + t * a.ldy + ch_row;
+                    if (in64) ch.template store<OUT, 32, true>(r, xs[acc] + t0, xz[acc] + t0, y, a.ldy, a.tokens - t);
+                    else ch.template store<OUT, 32, false>(r, xs[acc] + t0, xz[acc] + t0, y, a.ldy, a.tokens - t);
                 }
             }
             tc_fence_before();
@@ -477,6 +518,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(256, 1)
 }
 
 // ------------------------------------------------------------------ host side
+
+// What a call takes in cycles, roughly, by either kernel; measured over 24 to 515 tokens, 1024 to 14336 rows and 512 to
+// 16384 columns on 148 SMs.  A step of 128 k costs its copies, 2.8 cycles a row of 128 bytes with all SMs copying from L2
+// (540 cycles at 128 tokens a pair, 730 at 256, where the MMAs alone need 512), and some latency at least.  Wide tiles
+// start and end cheaper (5000 cycles against 9000, and 60 a token for the cluster's sums); narrow ones split k and so
+// keep SMs busy when there are few row tiles: 64 tokens x 4096 x 4096 8.8 us narrow, 10.7 wide; 128 tokens 12.2 and 11.1;
+// 128 tokens x 14336 x 4096 (k first) 22 and 28, x 4096 x 14336 18.1 and 15.0.
+static double wide_cycles(int64_t tiles, int pairs, int chunks, int bn) {
+    const double busy = std::min(1.0, static_cast<double>(tiles) / pairs);
+    const double step = std::max({460.0, 2.0 * bn, 2.85 * (kTileRows + bn / 2) * busy}) + 0.5 * bn;
+    return static_cast<double>((tiles + pairs - 1) / pairs) * chunks * step + 5000;
+}
+static double narrow_cycles(int64_t row_tiles, int split, int sms, int chunks, int bn) {
+    const int64_t ctas = row_tiles * split;
+    const double busy = std::min(1.0, static_cast<double>(ctas) / sms);
+    const double step = std::max(300.0, 2.85 * (kTileRows + bn) * busy);
+    return static_cast<double>((ctas + sms - 1) / sms) * ((chunks + split - 1) / split) * step + 9000 + (split > 1 ? 60.0 * bn : 0.0);
+}
 
 template <typename T>
 static const void *pick_quantize(int vecs) {
@@ -559,16 +618,28 @@ extern "C" int entro_matmul_i8(const int8_t *d_q, int64_t ldq, const float *d_x_
     a.chunks = static_cast<int>((cols + kChunkBytes - 1) / kChunkBytes);
     a.tx_extra = test_tx_extra();
     const uint32_t types = kAccS32 | (w_type == ENTRO_S8 ? kAS8 : kAU8) | kBS8;
-    const bool narrow = tokens <= 256;
+    // wide tiles: the width whose waves cost least
+    const int pairs = di.sms / 2;
+    const int64_t wide_rows = (rows + 255) / 256;
+    double wide_cost = 1e300;
+    int wide_bn = 256;
+    for (int bn = 256; bn >= 32; bn -= 32) {
+        const double c = wide_cycles((tokens + bn - 1) / bn * wide_rows, pairs, a.chunks, bn);
+        if (c < wide_cost) wide_cost = c, wide_bn = bn;
+    }
+    // one narrow tile of all tokens: k split as long as that fills SMs
+    const int narrow_bn = static_cast<int>((tokens + 15) / 16 * 16);
+    const int64_t narrow_rows = (rows + kTileRows - 1) / kTileRows;
+    int split = 1;
+    while (split < 8 && split * 2 <= a.chunks && narrow_rows * split * 2 <= di.sms) split *= 2;
+    const bool narrow = narrow_bn <= 256 && narrow_rows <= 65535 && narrow_cycles(narrow_rows, split, di.sms, a.chunks, narrow_bn) < wide_cost;
     size_t smem;
     dim3 grid;
     unsigned cluster, threads;
     const void *fn;
     if (narrow) {
-        a.bn = static_cast<int>((tokens + 15) / 16 * 16);
-        a.row_tiles = static_cast<int>((rows + kTileRows - 1) / kTileRows);
-        int split = 1;
-        while (split < 8 && split * 2 <= a.chunks && a.row_tiles * split * 2 <= di.sms) split *= 2;
+        a.bn = narrow_bn;
+        a.row_tiles = static_cast<int>(narrow_rows);
         const int stage = kABytes + a.bn * kChunkBytes;
         a.stages = std::min(8, 100 * 1024 / stage < 3 ? 200 * 1024 / stage : 100 * 1024 / stage);
         a.tmem_cols = 32;
@@ -582,16 +653,9 @@ extern "C" int entro_matmul_i8(const int8_t *d_q, int64_t ldq, const float *d_x_
         fn = y_type == ENTRO_F32 ? reinterpret_cast<const void *>(product_narrow_kernel<OUT_F32>)
              : y_type == ENTRO_BF16 ? reinterpret_cast<const void *>(product_narrow_kernel<OUT_BF16T>)
                                     : reinterpret_cast<const void *>(product_narrow_kernel<OUT_F16T>);
-        if (a.row_tiles > 65535) return ENTRO_E_LIMIT;
     } else {
-        // the tile width whose waves cost least (a wave of the pairs takes about bn, and a fixed part)
-        const int pairs = di.sms / 2;
-        a.row_tiles = static_cast<int>((rows + 255) / 256);
-        int64_t best = INT64_MAX;
-        for (int bn = 256; bn >= 128; bn -= 32) {
-            const int64_t tiles = (tokens + bn - 1) / bn * a.row_tiles, cost = (tiles + pairs - 1) / pairs * (bn + 16);
-            if (cost < best) best = cost, a.bn = bn;
-        }
+        a.row_tiles = static_cast<int>(wide_rows);
+        a.bn = wide_bn;
         a.token_tiles = static_cast<int>((tokens + a.bn - 1) / a.bn);
         const int stage = kABytes + a.bn / 2 * kChunkBytes;
         a.stages = std::min(8, 200 * 1024 / stage);

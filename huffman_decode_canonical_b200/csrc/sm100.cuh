@@ -275,6 +275,35 @@ struct Half<__half> {
     static constexpr uint32_t kExp = 0x7C007C00u;
 };
 
+// ------------------------------------------------------------------ pairs of fp32 numbers
+
+__device__ __forceinline__ uint64_t pair(uint32_t lo, uint32_t hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+    return r;
+}
+__device__ __forceinline__ uint64_t pair(float lo, float hi) { return pair(__float_as_uint(lo), __float_as_uint(hi)); }
+__device__ __forceinline__ float2 halves(uint64_t v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
 // ------------------------------------------------------------------ 8-bit codes
 
 // Codes of numbers that share a scale, from the largest magnitude a among them
@@ -299,15 +328,21 @@ struct BlockCode {
         by = 127.0f * pre;
     }
     __device__ __forceinline__ float scale() const { return finite ? __fdiv_rn(amax, 127.0f) : __int_as_float(0x7FC00000); }
-    __device__ __forceinline__ int one(float x) const {
-        const float t = __fmul_rn(__fmul_rn(x, by), rcp), c = __fmul_rn(t, 17.0f);
-        return finite ? __float2int_rn(__fsub_rn(c, __fsub_rn(c, t))) : 0;
+    // The low byte of each half of the result's bits is a code: the rounded quotient plus 1.5 x 2^23.
+    __device__ __forceinline__ uint64_t two(float x, float y) const {
+        const uint64_t t = mul2(mul2(pair(x, y), pair(by, by)), pair(rcp, rcp)), c = mul2(t, pair(17.0f, 17.0f)), minus = pair(-1.0f, -1.0f);
+        return add2(fma2(fma2(t, minus, c), minus, c), pair(12582912.0f, 12582912.0f));  // c - (c - t), then to a whole number
     }
+    __device__ __forceinline__ int one(float x) const { return finite ? static_cast<int8_t>(static_cast<uint32_t>(two(x, x))) : 0; }
     __device__ __forceinline__ uint32_t four(uint32_t lo, uint32_t hi) const {
         const float2 p = Half<T>::widen(lo), r = Half<T>::widen(hi);
-        return __byte_perm(__byte_perm(one(p.x), one(p.y), 0x0040), __byte_perm(one(r.x), one(r.y), 0x0040), 0x5410);
+        const uint64_t a = two(p.x, p.y), b = two(r.x, r.y);
+        const uint32_t ab = __byte_perm(static_cast<uint32_t>(a), static_cast<uint32_t>(a >> 32), 0x0040);
+        return __byte_perm(ab, __byte_perm(static_cast<uint32_t>(b), static_cast<uint32_t>(b >> 32), 0x0040), 0x5410);
     }
-    __device__ __forceinline__ uint2 eight(uint4 v) const { return make_uint2(four(v.x, v.y), four(v.z, v.w)); }
+    __device__ __forceinline__ uint2 eight(uint4 v) const {
+        return finite ? make_uint2(four(v.x, v.y), four(v.z, v.w)) : make_uint2(0, 0);
+    }
 };
 
 }  // namespace sm100
