@@ -38,6 +38,7 @@ struct AppendArgs {
     int32_t *status;
     int64_t tokens, table_stride;
     int batch, table_width;
+    int heads;  // key heads that a CTA takes, one after the other
 };
 
 constexpr int kAppendThreads = 128;
@@ -98,26 +99,28 @@ __device__ __forceinline__ bool find_block(const AppendArgs &a, int64_t item, in
     return false;
 }
 
-// One CTA a (block, head, keys or values).  Bound by memory: 2 bytes of each
-// new element in, 1 (or 2, in the tail) out.
+// One CTA a (block, some heads, keys or values): finding the block costs as much as coding a small one, so
+// long calls take four heads a CTA.  Bound by memory: 2 bytes of each new element in, 1 (or 2, in the tail) out.
 template <typename T, int D, int P>
 __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs a) {
     constexpr int kVecs = P * D / 8, kMine = (kVecs + kAppendThreads - 1) / kAppendThreads, kRow = D / 8;
     __shared__ uint32_t red[kAppendThreads / 32];
     int b, block, begin, n, start;
     if (!find_block(a, blockIdx.x, b, block, begin, n, start)) return;
-    const int tid = threadIdx.x, h = blockIdx.y, kind = blockIdx.z, end = start + n;
+    const int tid = threadIdx.x, kind = blockIdx.z, end = start + n;
     const int slot = a.slot_of ? a.slot_of[b] : b;
     const int first = start / P, last_open = end % P ? end / P : -1;  // the block that stays open, if any
-    T *tail = static_cast<T *>(a.c.tail[kind]) + (static_cast<int64_t>(slot) * a.c.kv + h) * (P * D);
-    const T *in = static_cast<const T *>(a.in[kind]) + begin * a.in_token[kind] + h * a.in_head[kind];
     // When the first block's older tokens are in the tail, its CTA writes the open block's
     // tokens over them after it has read them; otherwise the open block's own CTA does.
     const bool older = start % P != 0;
+    if (block == last_open && block != first && older) return;
+    const int page = block != last_open ? a.table[b * a.table_stride + block] : 0;
+    const bool ok = page >= 0 && page < a.c.pages;
+    if (!ok) set_status(a.status, ENTRO_E_INVAL);
+    for (int h = blockIdx.y * a.heads; h < min((blockIdx.y + 1) * a.heads, static_cast<unsigned>(a.c.kv)); h++) {
+    T *tail = static_cast<T *>(a.c.tail[kind]) + (static_cast<int64_t>(slot) * a.c.kv + h) * (P * D);
+    const T *in = static_cast<const T *>(a.in[kind]) + begin * a.in_token[kind] + h * a.in_head[kind];
     if (block != last_open) {
-        const int page = a.table[b * a.table_stride + block];
-        const bool ok = page >= 0 && page < a.c.pages;
-        if (!ok) set_status(a.status, ENTRO_E_INVAL);
         uint4 v[kMine];
         uint32_t m = 0;
 #pragma unroll
@@ -145,10 +148,8 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs
             }
             if (tid == 0) a.c.scale[kind][static_cast<int64_t>(page) * a.c.kv + h] = code.scale();
         }
-        if (block != first || !older || last_open < 0) return;
-        __syncthreads();  // the older tokens have been read
-    } else if (block != first && older) {
-        return;
+        __syncthreads();  // the older tokens have been read (and the maxima)
+        if (block != first || !older || last_open < 0) continue;
     }
     // the open block's new tokens into the tail
     const int from = max(start, last_open * P);
@@ -156,6 +157,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs
         const int pos = from + u / kRow, x = u % kRow * 8;
         *reinterpret_cast<uint4 *>(tail + pos % P * D + x) =
             __ldg(reinterpret_cast<const uint4 *>(in + (pos - start) * a.in_token[kind] + x));
+    }
     }
 }
 
@@ -197,24 +199,36 @@ __global__ void __launch_bounds__(256) read_kernel(const ReadArgs a) {
         if (lane == 0) set_status(a.status, ENTRO_E_INVAL);
         return;
     }
-    constexpr int kRow = D / 8;
     const int off = pos & (P - 1);
-    for (int u = lane; u < 2 * a.c.kv * kRow; u += 32) {
-        const int x = u % kRow * 8, row = u / kRow, kind = row >= a.c.kv, h = row - kind * a.c.kv;
-        T *out = static_cast<T *>(a.out[kind]) + t * a.out_token[kind] + h * a.out_head[kind] + x;
-        if (open) {
+    if (open) {
+        constexpr int kRow = D / 8;
+        for (int u = lane; u < 2 * a.c.kv * kRow; u += 32) {
+            const int x = u % kRow * 8, row = u / kRow, kind = row >= a.c.kv, h = row - kind * a.c.kv;
             const T *tail = static_cast<const T *>(a.c.tail[kind]) + ((static_cast<int64_t>(slot) * a.c.kv + h) * P + off) * D + x;
-            *reinterpret_cast<uint4 *>(out) = __ldg(reinterpret_cast<const uint4 *>(tail));
-            continue;
+            *reinterpret_cast<uint4 *>(static_cast<T *>(a.out[kind]) + t * a.out_token[kind] + h * a.out_head[kind] + x) =
+                __ldg(reinterpret_cast<const uint4 *>(tail));
         }
+        return;
+    }
+    constexpr int kRow = D / 16;
+#pragma unroll 4
+    for (int u = lane; u < 2 * a.c.kv * kRow; u += 32) {
+        const int x = u % kRow * 16, row = u / kRow, kind = row >= a.c.kv, h = row - kind * a.c.kv;
         const int64_t at = static_cast<int64_t>(page) * a.c.kv + h;
         const float s = __ldg(a.c.scale[kind] + at);
-        const uint2 c = __ldg(reinterpret_cast<const uint2 *>(a.c.codes[kind] + (at * P + off) * D + x));
-        auto two = [&](uint32_t w, int i) {
-            return Half<T>::pack(static_cast<float>(static_cast<int8_t>(w >> (16 * i))) * s,
-                                 static_cast<float>(static_cast<int8_t>(w >> (16 * i + 8))) * s);
-        };
-        *reinterpret_cast<uint4 *>(out) = make_uint4(two(c.x, 0), two(c.x, 1), two(c.y, 0), two(c.y, 1));
+        const uint4 c = __ldg(reinterpret_cast<const uint4 *>(a.c.codes[kind] + (at * P + off) * D + x));
+        const uint32_t w[4] = {c.x ^ 0x80808080u, c.y ^ 0x80808080u, c.z ^ 0x80808080u, c.w ^ 0x80808080u};
+        uint32_t o[8];
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+            // 2^23 + (code + 128) has the code's byte as its low bits
+            const uint32_t lo = __byte_perm(w[i / 2], 0x4B000000u, 0x7540 + i % 2 * 2), hi = __byte_perm(w[i / 2], 0x4B000000u, 0x7541 + i % 2 * 2);
+            const float2 v = halves(mul2(add2(pair(lo, hi), pair(-8388736.0f, -8388736.0f)), pair(s, s)));
+            o[i] = Half<T>::pack(v.x, v.y);
+        }
+        uint4 *out = reinterpret_cast<uint4 *>(static_cast<T *>(a.out[kind]) + t * a.out_token[kind] + h * a.out_head[kind] + x);
+        out[0] = make_uint4(o[0], o[1], o[2], o[3]);
+        out[1] = make_uint4(o[4], o[5], o[6], o[7]);
     }
 }
 
@@ -893,9 +907,10 @@ extern "C" int entro_kv_append(const entro_kv_cache *cache, const void *d_k, int
     // blocks that get new tokens: each has one at least, and a sequence's n reach at most (n - 2) / P + 2
     const int P = 1 << a.c.log_page;
     const int64_t items = std::min<int64_t>(tokens, (tokens + static_cast<int64_t>(batch) * (P - 2)) / P + batch);
+    a.heads = items * a.c.kv >= 8192 ? 4 : 1;
     const void *fn = ENTRO_BY_TYPE(cache, ENTRO_APPEND, a.c.log_page);
     void *args[] = {&a};
-    const cudaError_t e = launch_ex(fn, dim3(static_cast<unsigned>(items), a.c.kv, 2), kAppendThreads, 0,
+    const cudaError_t e = launch_ex(fn, dim3(static_cast<unsigned>(items), (a.c.kv + a.heads - 1) / a.heads, 2), kAppendThreads, 0,
                                     static_cast<cudaStream_t>(stream), 1, false, args);
     return e == cudaSuccess ? ENTRO_OK : cuda_fail(e, "entro_kv_append");
 }
