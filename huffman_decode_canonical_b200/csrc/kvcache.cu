@@ -473,7 +473,9 @@ struct Running {
 // where the (sequence, head) changes; a piece that covers all of its sequence and
 // head is finished here, others leave (m, l, o) behind for the join.  Bound by
 // reading the codes (2 D bytes of a token and key head).
-constexpr int kSteps = 3;  // a warp's steps in flight: with 16 warps on an SM three times what the memory's latency needs
+// A warp's steps in flight, the one at work among them.  Two with 16 warps on an SM keep memory as busy as it gets
+// (48 sequences of 16000 tokens, 8 key heads of 128: 191 us; three 199, four 227).
+constexpr int kSteps = 2;
 
 template <int D>
 constexpr int attend_smem() {
@@ -746,17 +748,16 @@ __global__ void __launch_bounds__(kAttendThreads, 4) attend_kernel(const AttendA
     }
 }
 
-// Joins the pieces of each (sequence, key head, chunk): a CTA each.  Sequences
+// Joins the pieces of each sequence and query head: a CTA each, its two halves taking every other piece.  Sequences
 // without tokens get zeros.
 template <typename T, int D>
 __global__ void __launch_bounds__(kAttendThreads) join_kernel(const AttendArgs a) {
-    const int tid = threadIdx.x, cols = a.c.kv * a.chunks;
-    const int seq = static_cast<int>(blockIdx.x / cols), col = static_cast<int>(blockIdx.x % cols);
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, heads = a.c.kv * a.group, cols = a.c.kv * a.chunks;
+    const int seq = static_cast<int>(blockIdx.x) / heads, head = static_cast<int>(blockIdx.x) % heads;
+    const int col = head / a.group * a.chunks + head % a.group / kHeads, in_chunk = head % a.group % kHeads;
     int got;
     uint32_t before;
     const uint32_t total = scan_batch(a, got, before, [&](int b, uint32_t, uint32_t, uint32_t) { return b == seq; }) * cols;
-    const int h = col / a.chunks, head0 = h * a.group + col % a.chunks * kHeads;
-    const int heads = min(kHeads, a.group - col % a.chunks * kHeads);
     const int tiles = (clean_len(a, seq, true) + kTile - 1) / kTile;
     const Shares shares(total, a.ctas);
     const uint32_t t0 = before * cols + col * tiles;
@@ -767,66 +768,51 @@ __global__ void __launch_bounds__(kAttendThreads) join_kernel(const AttendArgs a
     }
     wait_for_prior_grid();  // (the lengths above are no work of the grid before)
     if (tiles > 0 && first == last) return;  // one CTA had it all
-    // 64 pieces at a time: all their maxima and sums first (a piece's weight is 2^(its maximum - the largest)), then
-    // their outputs, with nothing between the loads
-    constexpr int kPieces = 64, kMine = kHeads * (D / 2) / kAttendThreads;
-    __shared__ float weight[kHeads][kPieces], rescale[kHeads], sum[kHeads], most[kHeads];
-    const int warp = tid / 32, lane = tid % 32;
-    auto row_of = [&](int i, int head) { return a.work + ((static_cast<int64_t>(i) * 2 + (i == first)) * kHeads + head) * (D + 2); };
-    float2 o[kMine];
-#pragma unroll
-    for (int u = 0; u < kMine; u++) o[u] = make_float2(0.0f, 0.0f);
-    if (tid < kHeads) most[tid] = -INFINITY, sum[tid] = 0.0f;
-    __syncthreads();
-    const int pieces = tiles > 0 ? last - first + 1 : 0;
-    for (int i0 = 0; i0 < pieces; i0 += kPieces) {
+    // 64 pieces at a time: their maxima and sums first (a piece's weight is 2^(its maximum - the largest)), then their
+    // outputs, with nothing between the loads
+    constexpr int kPieces = 64;
+    __shared__ float weight[2][kPieces];
+    __shared__ float2 half_o[64];
+    auto row_of = [&](int i) { return a.work + ((static_cast<int64_t>(i) * 2 + (i == first)) * kHeads + in_chunk) * (D + 2); };
+    const int pieces = tiles > 0 ? last - first + 1 : 0, half = tid / 64, d = tid % 64 * 2;
+    float most = -INFINITY, sum = 0.0f;
+    float2 o = make_float2(0.0f, 0.0f);
+    for (int i0 = 0, turn = 0; i0 < pieces; i0 += kPieces, turn ^= 1) {
         const int n = min(kPieces, pieces - i0);
-        for (int head = warp; head < heads; head += kAttendThreads / 32) {
-            float2 ml[2];
+        float2 ml[2];  // (every warp looks at all of them: no barrier between this and what follows)
 #pragma unroll
-            for (int x = 0; x < 2; x++)
-                ml[x] = lane + 32 * x < n ? *reinterpret_cast<const float2 *>(row_of(first + i0 + lane + 32 * x, head)) : make_float2(-INFINITY, 0.0f);
-            float m = fmaxf(ml[0].x, ml[1].x);
-            for (int x = 16; x; x /= 2) m = fmaxf(m, __shfl_xor_sync(~0u, m, x));
-            const float was = most[head], now = fmaxf(was, m);
-            float l = 0.0f;
+        for (int x = 0; x < 2; x++)
+            ml[x] = lane + 32 * x < n ? *reinterpret_cast<const float2 *>(row_of(first + i0 + lane + 32 * x)) : make_float2(-INFINITY, 0.0f);
+        float m = fmaxf(ml[0].x, ml[1].x);
+        for (int x = 16; x; x /= 2) m = fmaxf(m, __shfl_xor_sync(~0u, m, x));
+        const float now = fmaxf(most, m), f = most == now ? 1.0f : ex2(most - now);
+        float l = 0.0f;
 #pragma unroll
-            for (int x = 0; x < 2; x++) {
-                const float w = ml[x].x == now ? 1.0f : ex2(ml[x].x - now);
-                weight[head][lane + 32 * x] = w;
-                l += w * ml[x].y;
-            }
-            for (int x = 16; x; x /= 2) l += __shfl_xor_sync(~0u, l, x);
-            __syncwarp();
-            if (lane == 0) {
-                const float f = was == now ? 1.0f : ex2(was - now);
-                rescale[head] = f;
-                sum[head] = sum[head] * f + l;
-                most[head] = now;
-            }
+        for (int x = 0; x < 2; x++) {
+            const float w = ml[x].x == now ? 1.0f : ex2(ml[x].x - now);
+            if (warp == 0) weight[turn][lane + 32 * x] = w;
+            l += w * ml[x].y;
         }
-        __syncthreads();
-#pragma unroll
-        for (int u = 0; u < kMine; u++) {
-            const int unit = u * kAttendThreads + tid, head = unit / (D / 2), d = unit % (D / 2) * 2;
-            if (head >= heads) break;
-            o[u].x *= rescale[head], o[u].y *= rescale[head];
+        for (int x = 16; x; x /= 2) l += __shfl_xor_sync(~0u, l, x);
+        sum = sum * f + l;
+        most = now;
+        __syncthreads();  // (two turns' weights: a warp may be one ahead)
+        o.x *= f, o.y *= f;
+        if (d < D) {
 #pragma unroll 8
-            for (int i = 0; i < n; i++) {
-                const float2 v = *reinterpret_cast<const float2 *>(row_of(first + i0 + i, head) + 2 + d);
-                o[u].x += weight[head][i] * v.x;
-                o[u].y += weight[head][i] * v.y;
+            for (int i = half; i < n; i += 2) {
+                const float2 v = *reinterpret_cast<const float2 *>(row_of(first + i0 + i) + 2 + d);
+                o.x += weight[turn][i] * v.x;
+                o.y += weight[turn][i] * v.y;
             }
         }
-        __syncthreads();
     }
-#pragma unroll
-    for (int u = 0; u < kMine; u++) {
-        const int unit = u * kAttendThreads + tid, head = unit / (D / 2), d = unit % (D / 2) * 2;
-        if (head >= heads) break;
-        const float by = sum[head] == 0.0f ? 0.0f : 1.0f / sum[head];
-        T *out = static_cast<T *>(a.out) + seq * a.out_token + (head0 + head) * a.out_head + d;
-        *reinterpret_cast<uint32_t *>(out) = Half<T>::pack(o[u].x * by, o[u].y * by);
+    if (half == 1) half_o[tid - 64] = o;
+    __syncthreads();
+    if (half == 0 && d < D) {
+        const float by = sum == 0.0f ? 0.0f : 1.0f / sum;
+        T *out = static_cast<T *>(a.out) + seq * a.out_token + head * a.out_head + d;
+        *reinterpret_cast<uint32_t *>(out) = Half<T>::pack((o.x + half_o[tid].x) * by, (o.y + half_o[tid].y) * by);
     }
 }
 
@@ -971,7 +957,9 @@ extern "C" int entro_kv_attend(const entro_kv_cache *cache, const void *d_q, int
     const int64_t columns = static_cast<int64_t>(batch) * a.c.kv * a.chunks;
     // all tiles are counted in 32 bits
     if (columns * (((static_cast<int64_t>(table_width) + 1) << a.c.log_page) / kTile + 1) > INT32_MAX) return ENTRO_E_LIMIT;
-    a.join_early = columns <= a.ctas / 4;  // a CTA on each SM at most, beside the four that are there
+    const int64_t joins = static_cast<int64_t>(batch) * heads;
+    if (joins > INT32_MAX) return ENTRO_E_LIMIT;
+    a.join_early = joins <= a.ctas / 4;  // a CTA on each SM at most, beside the four that are there
     const size_t smem = cache->head_dim == 64 ? attend_smem<64>() : cache->head_dim == 96 ? attend_smem<96>() : attend_smem<128>();
     const void *fn = ENTRO_BY_TYPE(cache, ENTRO_ATTEND);
     int dev = 0;
@@ -983,6 +971,6 @@ extern "C" int entro_kv_attend(const entro_kv_cache *cache, const void *d_q, int
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     e = launch_ex(fn, dim3(a.ctas), kAttendThreads, smem, st, 1, false, args);
     if (e == cudaSuccess)
-        e = launch_ex(ENTRO_BY_TYPE(cache, ENTRO_JOIN), dim3(static_cast<unsigned>(columns)), kAttendThreads, 0, st, 1, a.join_early, args);
+        e = launch_ex(ENTRO_BY_TYPE(cache, ENTRO_JOIN), dim3(static_cast<unsigned>(joins)), kAttendThreads, 0, st, 1, a.join_early, args);
     return e == cudaSuccess ? ENTRO_OK : cuda_fail(e, "entro_kv_attend");
 }
