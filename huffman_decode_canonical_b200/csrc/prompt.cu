@@ -4,15 +4,21 @@
 //   o_i = sum_{j <= i + klen - qlen} p_ij v_j,  p_i = softmax_j(scale q_i . k_j)
 //
 // A CTA takes 256 queries of one head as two tiles of 128 rows and walks the
-// keys in tiles of 128.  Each query tile has its scores S, whose room its
-// weights P then take, and its output O in TMEM (lane = query row): S = Q K^T
-// from shared memory, P V with P read from TMEM.  One warp issues all MMAs, one
-// the TMA copies; four warps for each query tile take the softmax, a row a
-// thread, so that one tile's softmax runs beside the other's MMAs.  The reference
-// maximum of a row is only raised when a score passes it by 2^8 (any reference
-// gives the same quotient), so O is rarely rescaled.  Bound by the exponentials
-// and the MMAs about alike: 128 x 128 scores take 16384 exponentials (16 a clock
-// and SM) and 2 x 128 x 128 x D multiply-adds (4096 a clock).
+// keys in tiles of 64 to 128 (below), then goes on with another block of queries.
+// S = Q K^T from shared memory and O += P V with P read from TMEM are
+// tcgen05.mma; S, P and O are in TMEM (lane = query row).  A warp issues each query
+// tile's MMAs, one finds the work and issues the TMA copies, one looks over values
+// that are partly hidden, and four warps for each query tile take the softmax, a
+// row a thread.  The reference maximum of a row is only raised when a score passes
+// it by 2^8 (any reference gives the same quotient), so O is rarely rescaled.
+// Bound by the exponentials and the MMAs about alike at 128 channels (128 x 128
+// scores take 16384 exponentials, 16 a clock and SM, and 2 x 128 x 128 x D
+// multiply-adds, 4096 a clock), by the exponentials and the instructions around
+// them at 64 and 96.  8192 tokens, 32 heads of 128 over 8: 452 us in a short run (1215
+// TFLOP/s), 536 us in a long one at the power limit; 4096 tokens, 32 heads of 64: 108 us
+// (638); 5 prompts of 6011 tokens in all, 32 heads of 96: 106 us (627).  Taking a part of
+// the exponentials by a polynomial instead, or looking for the maximum only after a
+// weight came out too large, was slower (463 us -> 489 to 518, and 562).
 //
 // What the mask hides must not count, whatever it holds.  Scores are replaced one
 // by one.  Values of a tile that some row must not see are looked over in shared
