@@ -3,8 +3,8 @@
 Every step of the path -- quantization and Huffman coding on the host, decoding,
 dequantization and the fused GEMV on the GPU -- runs inside ``libentro.so``;
 this module turns numpy / torch objects into pointers and sizes for the C ABI
-declared in ``include/entro.h`` and turns return codes into exceptions.
-PyTorch is used for device memory and streams only.  There is no fallback:
+declared in ``include/entro.h`` and turns return codes into exceptions (the
+operators' usual calls do so in ``csrc/binding.cpp``).  PyTorch is used for device memory and streams only.  There is no fallback:
 importing this package fails when the shared library is missing, and device
 calls need a CUDA GPU.
 
@@ -22,6 +22,8 @@ from typing import List, NamedTuple, Optional, Sequence, Union
 
 import numpy as np
 import torch
+
+from . import _binding as _fast  # built with the library (build.py)
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libentro.so")
@@ -121,6 +123,10 @@ def _load() -> ctypes.CDLL:
 
 
 _lib = _load()
+# The usual calls of the operators around the coded weights, checked and made without the interpreter's part: each
+# returns None for anything that is not the plain valid case, and the function here goes on.
+_fast.init(*(ctypes.cast(getattr(_lib, f), ctypes.c_void_p).value for f in (
+    "entro_quantize_tokens", "entro_matmul_i8", "entro_attention_prompt", "entro_kv_append", "entro_kv_read", "entro_kv_attend")))
 
 
 def lib() -> ctypes.CDLL:
@@ -420,6 +426,10 @@ class QuantTokens(NamedTuple):
 
 def quantize_tokens(x: torch.Tensor, stream: Optional[torch.cuda.Stream] = None) -> QuantTokens:
     """bf16 or fp16 [tokens, cols] (any row stride) to codes 127 x / max|x| of each token, with scale max|x| / 127."""
+    if stream is None:
+        done = _fast.quantize_tokens(x)
+        if done is not None:
+            return QuantTokens._make(done)
     if x.dtype not in (torch.bfloat16, torch.float16) or x.dim() != 2 or x.shape[1] < 1 or x.stride(1) != 1:
         raise ValueError("x must be a bf16 or fp16 [tokens, cols] tensor with adjacent columns")
     index = x.get_device()
@@ -446,6 +456,10 @@ def matmul_i8(x: QuantTokens, w: torch.Tensor, w_scale: Union[float, torch.Tenso
     w uint8 or int8 [rows, cols], adjacent columns, rows a multiple of 16 bytes apart; w_scale a number or fp32 [rows];
     w_zero a whole number, int32 [rows] or None (0).  out: fp32, bf16 or fp16 [tokens, rows] with adjacent columns."""
     q, scale, total = x
+    if stream is None and out is None:
+        done = _fast.matmul_i8(q, scale, total, w, w_scale, w_zero, _TYPES.get(out_dtype), status)
+        if done is not None:
+            return done
     if w.dtype not in (torch.uint8, torch.int8) or w.dim() != 2 or w.shape[1] < 1 or w.stride(1) != 1:
         raise ValueError("w must be a uint8 or int8 [rows, cols] tensor with adjacent columns")
     rows, cols = w.shape
@@ -519,6 +533,10 @@ def attention_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqle
     begin, cu_keys its keys (None: as the queries); a sequence's last query sees its last key, so queries that continue a
     context give their keys with it.  scale: 1 / sqrt(head_dim) by default.  Rows of no sequence are left as they are (give
     `out` to keep theirs)."""
+    if stream is None and out is None:
+        done = _fast.attention_prompt(q, k, v, cu_seqlens, cu_keys, scale, status)
+        if done is not None:
+            return done
     if q.dtype not in (torch.bfloat16, torch.float16) or q.dim() != 3 or k.dim() != 3:
         raise ValueError("q, k and v must be bf16 or fp16 [tokens, heads, head_dim] tensors")
     tokens, heads, dim = q.shape
@@ -598,6 +616,7 @@ class KVCache:
         self._c = _KVCache(k_codes.data_ptr(), v_codes.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), k_tail.data_ptr(),
                            v_tail.data_ptr(), pages, slots, kv, page, dim, _TYPES[dtype])
         self._ref = ctypes.byref(self._c)
+        self._address = ctypes.addressof(self._c)
         self._work_bytes = None
 
     @classmethod
@@ -630,6 +649,8 @@ class KVCache:
                stream: Optional[torch.cuda.Stream] = None) -> None:
         """Packed new tokens k, v [tokens, kv_heads, head_dim] to their sequences; cu_seqlens int32 [batch + 1] says where
         each sequence's begin, lens counts them already.  No page or slot may be written for two sequences."""
+        if stream is None and _fast.kv_append(self._address, self._index, k, v, cu_seqlens, page_table, lens, slots, status):
+            return
         ks, vs = _rows(k, "k", self.dtype, self.kv_heads, self.head_dim), _rows(v, "v", self.dtype, self.kv_heads, self.head_dim)
         tokens = k.shape[0]
         if tokens != v.shape[0]:
@@ -651,6 +672,10 @@ class KVCache:
              out: Optional[tuple] = None, status: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None):
         """(k, v) [tokens, kv_heads, head_dim]: all tokens of the sequences, packed; sequence b holds
         cu_seqlens[b + 1] - cu_seqlens[b] of them."""
+        if stream is None and out is None:
+            done = _fast.kv_read(self._address, self._index, page_table, cu_seqlens, tokens, slots, status)
+            if done is not None:
+                return done
         batch, width, stride = self._tables(page_table, slots)
         _vector(cu_seqlens, "cu_seqlens", torch.int32, batch + 1, "[batch + 1]")
         heads, dim = self.kv_heads, self.head_dim
@@ -678,6 +703,10 @@ class KVCache:
                stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
         """Attention of one token of each sequence, q [batch, heads, head_dim] (heads a multiple of kv_heads), over its
         cached tokens; scale: 1 / sqrt(head_dim) by default.  A sequence without tokens gets zeros."""
+        if stream is None and out is None and self._work_bytes is not None:
+            done = _fast.kv_attend(self._address, self._index, self._work_bytes, q, page_table, lens, slots, scale, status)
+            if done is not None:
+                return done
         heads, dim = q.shape[1] if q.dim() == 3 else 0, self.head_dim
         qs = _rows(q, "q", self.dtype, heads, dim)
         if heads < 1 or heads % self.kv_heads:

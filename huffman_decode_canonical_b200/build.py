@@ -1,4 +1,4 @@
-"""Build libentro.so in-tree with nvcc for sm_100a (B200).
+"""Build libentro.so in-tree with nvcc for sm_100a (B200), and the Python binding's extension module (_binding.so).
 
     python huffman_decode_canonical_b200/build.py [--verbose-ptxas]
 
@@ -19,30 +19,38 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libentro.so")
 OBJECTS = os.path.join(HERE, "_build")
+BINDING = os.path.join(HERE, "_binding.so")
+BINDING_SOURCE = os.path.join(CSRC, "binding.cpp")
 SOURCES = [os.path.join(CSRC, f) for f in ("decode.cu", "product.cu", "prompt.cu", "kvcache.cu", "encoder.cpp", "launch.cpp")]
 HEADERS = sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".h", ".cuh"))) + [
     os.path.join(ROOT, "include", "entro.h")]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
 
-def _stale() -> bool:
-    if not os.path.exists(LIB):
-        return True
-    t = os.path.getmtime(LIB)
-    return any(os.path.getmtime(p) > t for p in SOURCES + HEADERS)
+def _stale(target: str, sources) -> bool:
+    return not os.path.exists(target) or any(os.path.getmtime(p) > os.path.getmtime(target) for p in sources)
 
 
 def _object(src: str) -> str:
     return os.path.join(OBJECTS, os.path.basename(src) + ".o")
 
 
-def _outdated(src: str) -> bool:
-    obj = _object(src)
-    return not os.path.exists(obj) or any(os.path.getmtime(p) > os.path.getmtime(obj) for p in [src] + HEADERS)
+def _binding_command(target: str):
+    """The extension module over torch's tensors (host code only)."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+    includes = [sysconfig.get_paths()["include"], os.path.join(ROOT, "include")] + cpp_extension.include_paths("cuda")
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    return ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+            *[f"-I{p}" for p in includes], BINDING_SOURCE, "-o", target, f"-L{libs}", "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-ltorch",
+            "-lc10_cuda", "-lc10"]
 
 
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
-    if not force and not _stale():
+    lib, binding = force or _stale(LIB, SOURCES + HEADERS), force or _stale(BINDING, [BINDING_SOURCE, os.path.join(ROOT, "include", "entro.h")])
+    if not lib and not binding:
         return LIB
     os.makedirs(OBJECTS, exist_ok=True)
     flags = ["-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo", "-O3", "-std=c++17",
@@ -52,10 +60,14 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
         flags = ["-Xptxas", "-v"] + flags
     running = []
     for src in SOURCES:  # the sources side by side
-        if force or _outdated(src):
+        if lib and (force or _stale(_object(src), [src] + HEADERS)):
             tmp = _object(src) + f".tmp{os.getpid()}"
             cmd = [NVCC] + flags + ["-c", "-o", tmp, src]
             running.append((cmd, tmp, _object(src), subprocess.Popen(cmd)))
+    if binding:
+        tmp = BINDING + f".tmp{os.getpid()}"
+        cmd = _binding_command(tmp)
+        running.append((cmd, tmp, BINDING, subprocess.Popen(cmd)))
     bad = None
     for cmd, tmp, obj, p in running:
         if p.wait() != 0:
@@ -64,6 +76,8 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
             os.replace(tmp, obj)
     if bad:
         raise subprocess.CalledProcessError(*bad)
+    if not lib:
+        return LIB
     tmp = LIB + f".tmp{os.getpid()}"
     subprocess.check_call([NVCC, "-gencode", "arch=compute_100a,code=sm_100a", "-shared", "-o", tmp]
                           + [_object(s) for s in SOURCES] + ["-lpthread"])
