@@ -4,7 +4,7 @@
 //   o_i = sum_{j <= i + klen - qlen} p_ij v_j,  p_i = softmax_j(scale q_i . k_j)
 //
 // A CTA takes 256 queries of one head as two tiles of 128 rows and walks the
-// keys in tiles of 64 to 128 (below), then goes on with another block of queries.
+// keys in tiles of 64, then goes on with another block of queries.
 // S = Q K^T from shared memory and O += P V with P read from TMEM are
 // tcgen05.mma; S, P and O are in TMEM (lane = query row).  A warp issues each query
 // tile's MMAs, one finds the work and issues the TMA copies, one looks over values
@@ -14,11 +14,12 @@
 // Bound by the exponentials and the MMAs about alike at 128 channels (128 x 128
 // scores take 16384 exponentials, 16 a clock and SM, and 2 x 128 x 128 x D
 // multiply-adds, 4096 a clock), by the exponentials and the instructions around
-// them at 64 and 96.  8192 tokens, 32 heads of 128 over 8: 452 us in a short run (1215
-// TFLOP/s), 536 us in a long one at the power limit; 4096 tokens, 32 heads of 64: 108 us
-// (638); 5 prompts of 6011 tokens in all, 32 heads of 96: 106 us (627).  Taking a part of
-// the exponentials by a polynomial instead, or looking for the maximum only after a
-// weight came out too large, was slower (463 us -> 489 to 518, and 562).
+// them at 64 and 96.  8192 tokens, 32 heads of 128 over 8: 430 us in a short run (1280
+// TFLOP/s), about 520 in a long one at the power limit; 4096 tokens, 32 heads of 64: 119
+// us (577); 5 prompts of 6011 tokens in all, 32 heads of 96: 97 us (688).  Taking a part of
+// the exponentials by a polynomial instead, looking for the maximum only after a weight
+// came out too large, or fetching the next scores beside the exponentials was slower (in
+// an earlier form 463 us -> 489 to 518, 562, and 510).
 //
 // What the mask hides must not count, whatever it holds.  Scores are replaced one
 // by one.  Values of a tile that some row must not see are looked over in shared
@@ -51,18 +52,21 @@ constexpr int kPromptThreads = 384;    // 2 x 4 softmax warps, an MMA warp for e
 constexpr float kLazyLog2 = 8.0f;
 constexpr int kMarks = 8;              // barriers for masked value tiles, more than the ring holds
 
-// TMEM has 512 columns: two query tiles' scores (a column a key), weights (two keys a column) and outputs (a column a
-// channel).  With weights of their own the next scores do not wait for the last weights' product, so the softmax
-// warps always find scores ready; 128 keys leave room for that beside outputs of 64 channels, 96 beside 96, 64 beside 128.
+// TMEM has 512 columns: for each of two query tiles the scores (64 columns, a key each), two buffers of weights (32
+// columns, two keys each) and the output (a column a channel).  With weights apart from scores the next scores do not
+// wait for the last weights' product, so the softmax warps always find scores ready; with two buffers the weights do not
+// wait for it either (step j's scores come after the product of step j - 2 in the order of the MMAs).  That is room for 64
+// keys a tile at 128 channels; at 64 channels 128 keys were no faster (4096 tokens: 119 and 122 us) and worse for short
+// prompts (16 of 44 tokens, 32 heads: 17.4 and 12.5 us).
 template <int D>
 struct PromptShape {
-    static constexpr int kKeys = D == 64 ? 128 : D == 96 ? 96 : 64;  // keys of a tile
+    static constexpr int kKeys = 64;                           // keys of a tile
     static constexpr int kChunks = (D + 63) / 64;              // 64 channels each; 96 fill one and a half, the rest reads as zero
     static constexpr int kQChunk = kRows * 128, kChunk = kKeys * 128;  // bytes of a chunk (one TMA box)
     static constexpr int kQTile = kChunks * kQChunk, kTile = kChunks * kChunk;
     static constexpr int kStages = (220 * 1024 - 2 * kQTile) / kTile < 10 ? (220 * 1024 - 2 * kQTile) / kTile : 10;  // key and value tiles in flight
     static constexpr int kSmem = 1024 + 2 * kQTile + kStages * kTile;
-    static constexpr uint32_t kS = 0, kP = 2 * kKeys, kO = 3 * kKeys;  // TMEM columns: S0 S1 P0 P1 O0 O1
+    static constexpr uint32_t kS = 0, kP = 2 * kKeys, kO = 4 * kKeys;  // TMEM columns: S0 S1, P0 P0 P1 P1, O0 O1
     static_assert(kO + 2 * D <= 512 && kStages / 2 < kMarks && kStages >= 4 && kKeys % 32 == 0, "");
 };
 
@@ -213,7 +217,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(16) uint32_t reply[4];
     __shared__ PromptItem items[2];
-    __shared__ __align__(8) uint64_t bars[2 * kStages + 21 + 2 * kMarks];
+    __shared__ __align__(8) uint64_t bars[2 * kStages + 23 + 2 * kMarks];
     __shared__ uint32_t tmem_base;
     __shared__ int failed, special[4];
     const uint32_t base = (smem_u32(smem_raw) + 1023) & ~1023u, ring = base + 2 * Shape::kQTile;
@@ -223,7 +227,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     const uint32_t item_full = empty + 8 * kStages, item_empty = item_full + 16;  // item n in place n % 2
     const uint32_t q_full = item_empty + 16, q_empty = q_full + 8;          // the item's queries; (per tile) read for the last time
     const uint32_t s_full = q_empty + 16, s_read = s_full + 16;             // per tile: scores; taken into registers
-    const uint32_t p_full = s_read + 16, p_read = p_full + 16;              // per tile: weights; multiplied
+    const uint32_t p_full = s_read + 16, p_read = p_full + 32;              // per tile: weights (per buffer); multiplied
     const uint32_t o_full = p_read + 16, o_empty = o_full + 16;             // per tile: the item's output; stored
     const uint32_t asked = o_empty + 16, turn = asked + 8, v_sent = turn + 8, v_seen = v_sent + 8 * kMarks;  // masked value tile g in place g % kMarks: on its way; looked over
     if (warp == 0) {
@@ -241,7 +245,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                 bar_init(q_empty + 8 * t, 1);
                 bar_init(s_full + 8 * t, 1);
                 bar_init(s_read + 8 * t, 4);
-                bar_init(p_full + 8 * t, 4);
+                bar_init(p_full + 16 * t, 4);
+                bar_init(p_full + 16 * t + 8, 4);
                 bar_init(p_read + 8 * t, 1);
                 bar_init(o_full + 8 * t, 1);
                 bar_init(o_empty + 8 * t, 4);
@@ -286,6 +291,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             PromptItem it;
             while (ok) {
                 const bool is = block >= 0 && find_item(a, block, it);
+                bool soon = false;
                 if (is || block < 0) {
                     if (block < 0) it.head = -1;
                     if (items_out >= 2) ok = __all_sync(~0u, bar_wait(item_empty + 8 * (items_out % 2), (items_out / 2 - 1) & 1));
@@ -297,6 +303,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                     items_out++;
                     if (block < 0) break;
                     const int n1 = it.key_tiles<kKeys>(1), n = max(it.key_tiles<kKeys>(0), n1), masked_from = it.masked_from<kKeys>();
+                    soon = n <= 4;
+                    if (soon && lane == 0) ask_next(smem_u32(reply), asked);
                     if (n > 0) {
                         if (elect_one()) {
                             const int kv = it.head / a.group, tiles = n1 > 0 ? 2 : 1;
@@ -325,10 +333,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                         g += max(0, n - masked_from);
                     }
                 }
-                // asked for only now, when all of this item's copies are on their way: a CTA that asks earlier takes work
-                // that another could begin sooner
+                // The next item is asked for only now, when all of this one's copies are on their way, unless that is short:
+                // a CTA that asks earlier takes work that another could begin sooner.
                 if (!ok) break;
-                if (lane == 0) ask_next(smem_u32(reply), asked);
+                if (!soon && lane == 0) ask_next(smem_u32(reply), asked);
                 if (!__all_sync(~0u, bar_wait(asked, answers++ & 1))) ok = false;
                 if (ok) block = next_block(smem_u32(reply));
                 __syncwarp();
@@ -378,7 +386,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             const int t = warp - 8;
             constexpr uint32_t kScores = kAccF32 | Half<T>::kA | Half<T>::kB | mma_shape(kRows, kKeys);
             constexpr uint32_t kValues = kAccF32 | Half<T>::kA | Half<T>::kB | kBMajorMN | mma_shape(kRows, D);
-            const uint32_t tS = tmem + Shape::kS + t * kKeys, tP = tmem + Shape::kP + t * (kKeys / 2), tO = tmem + Shape::kO + t * D;
+            const uint32_t tS = tmem + Shape::kS + t * kKeys, tP = tmem + Shape::kP + t * kKeys, tO = tmem + Shape::kO + t * D;
             PromptItem it;
             int i = 0, g = 0, queries = 0, steps = 0, outputs = 0, turns = 0;
             for (int n_item = 0; ok && take(n_item, it); n_item++) {
@@ -406,7 +414,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                     };
                     // The second tile begins when the first is through most of its first exponentials: side by side the
                     // two look for maxima together and then share the exponential unit, and leave that state only
-                    // slowly (128 keys of 64 channels: 3600 cycles in step, 2800 out of step).
+                    // slowly (2100 cycles a step in step, 1550 out of step).
                     ok = bar_wait(q_full, queries & 1) && (t == 0 || n0 == 0 || bar_wait(turn, turns & 1)) && scores(0);
                     for (int j = 0; j < n && ok; j++) {
                         if (j + 1 < n && !(ok = scores(j + 1))) break;
@@ -416,12 +424,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                             if (j >= masked_from && !(ok = bar_wait(v_seen + 8 * (gv % kMarks), gv / kMarks & 1))) break;
                             // the item before has taken its output away
                             if (j == 0 && outputs > 0 && !(ok = bar_wait(o_empty + 8 * t, (outputs - 1) & 1))) break;
-                            if (!(ok = bar_wait(p_full + 8 * t, (steps + j) & 1))) break;
+                            if (!(ok = bar_wait(p_full + 16 * t + (steps + j) % 2 * 8, (steps + j) / 2 & 1))) break;
                             tc_fence_after();
                             const uint32_t va = ring + (i + k) % kStages * Shape::kTile;
 #pragma unroll
                             for (int x = 0; x < kKeys / 16; x++)
-                                mma_f16_ta(tO, tP + x * 8, operand_desc(va + x * 2048, Shape::kChunk, 1024), kValues, j > 0 || x > 0);
+                                mma_f16_ta(tO, tP + (steps + j) % 2 * (kKeys / 2) + x * 8, operand_desc(va + x * 2048, Shape::kChunk, 1024), kValues, j > 0 || x > 0);
                             mma_commit(p_read + 8 * t);
                             if (j + 1 == nt) mma_commit(o_full + 8 * t);
                         }
@@ -442,7 +450,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
         const int t = warp / 4;
         const uint32_t lanes = static_cast<uint32_t>(warp % 4 * 32) << 16, st = tmem + Shape::kS + t * kKeys + lanes,
-                       pt = tmem + Shape::kP + t * (kKeys / 2) + lanes, ot = tmem + Shape::kO + t * D + lanes;
+                       pt = tmem + Shape::kP + t * kKeys + lanes, ot = tmem + Shape::kO + t * D + lanes;
         const float c = a.scale_log2;
         PromptItem it;
         int steps = 0, outputs = 0;
@@ -472,15 +480,14 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                 for (int x = 0; x < kKeys; x += 2) top[x / 2 % 4] = max3(top[x / 2 % 4], __uint_as_float(s[x]), __uint_as_float(s[x + 1]));
                 const float n_m = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
                 const bool raise = n_m * c > m * c + kLazyLog2;
-                bool read = steps + j == 0;  // the last weights, by their MMAs
                 if (__any_sync(~0u, raise)) {
                     const float f = raise ? exp2_fast((m - n_m) * c) : 1.0f;
                     if (raise) m = n_m;
                     l *= f;
                     if (j > 0) {
+                        // (O may be changed when the last weights have been multiplied, and none are before these are written)
                         ok = ok && bar_wait(p_read + 8 * t, (steps + j - 1) & 1);
                         __syncwarp();
-                        read = true;
                         tc_fence_after();
 #pragma unroll 1
                         for (int x = 0; x < D; x += 32) {
@@ -505,18 +512,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                     sum[y % 4] = add2(sum[y % 4], pair(e0, e1));
                     p[y] = Half<T>::pack(e0, e1);
                 }
-                if (!read) {
-                    ok = ok && bar_wait(p_read + 8 * t, (steps + j - 1) & 1);
-                    __syncwarp();
-                    tc_fence_after();
-                }
-                if (kKeys >= 64) tmem_st32(pt, p);
-                if (kKeys == 96) tmem_st16(pt + 32, p + 32);
-                if (kKeys == 128) tmem_st32(pt + 32, p + 32);
+                tmem_st32(pt + (steps + j) % 2 * (kKeys / 2), p);
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) bar_arrive(p_full + 8 * t);
+                if (lane == 0) bar_arrive(p_full + 16 * t + (steps + j) % 2 * 8);
                 const float2 both = halves(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])));
                 l += both.x + both.y;
             }
@@ -630,7 +630,7 @@ extern "C" int entro_attention_prompt(int32_t type, int32_t head_dim, const void
     if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
     size_t smem;
     const void *fn = type == ENTRO_BF16 ? pick_prompt<__nv_bfloat16>(head_dim, &smem) : pick_prompt<__half>(head_dim, &smem);
-    const int keys_of = head_dim == 64 ? PromptShape<64>::kKeys : head_dim == 96 ? PromptShape<96>::kKeys : PromptShape<128>::kKeys;
+    const int keys_of = PromptShape<64>::kKeys;  // (the same for all widths)
     int r = allow_smem(fn, dev);
     CUtensorMap q_map, k_map, v_map;
     if (r == ENTRO_OK) r = rows_map(&q_map, type, d_q, tokens, heads, head_dim, q_token, q_head, kRows);
