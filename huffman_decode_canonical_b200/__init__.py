@@ -400,9 +400,12 @@ class _on:
 
 
 def _check_inputs(index: int, tensors, names):
-    """Refuses what the kernels must not be given: tensors of other devices, or ones that ask for gradients."""
+    """Refuses what the kernels must not be given: tensors of other devices, or ones that ask for gradients; a status
+    that is no int32 word (the last one named so)."""
     if index < 0:
         raise ValueError("expected CUDA tensors")
+    if names[-1] == "status" and tensors[-1] is not None and (tensors[-1].dtype is not torch.int32 or tensors[-1].numel() < 1):
+        raise ValueError("status must be an int32 tensor")
     grad = torch.is_grad_enabled()
     for t in tensors:
         if t is not None and (t.get_device() != index or (grad and t.requires_grad)):
@@ -564,7 +567,7 @@ def attention_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqle
         if out.shape[0] != tokens:
             raise ValueError("out must have q's shape")
     scale = dim ** -0.5 if scale is None else float(scale)
-    if not 0.0 < scale < 3e38:
+    if not 0.0 < scale <= 2e38:
         raise ValueError("scale must be above 0 and finite")
     index = q.get_device()
     _check_inputs(index, (q, k, v, cu_seqlens, cu_keys, out, status), ("q", "k", "v", "cu_seqlens", "cu_keys", "out", "status"))
@@ -720,7 +723,7 @@ class KVCache:
             if out.shape[0] != batch:
                 raise ValueError("out must have q's shape")
         scale = dim ** -0.5 if scale is None else float(scale)
-        if not 0.0 < scale < 3e38:
+        if not 0.0 < scale <= 2e38:
             raise ValueError("scale must be above 0 and finite")
         index = self._index
         _check_inputs(index, (q, page_table, lens, slots, out, status), ("q", "page_table", "lens", "slots", "out", "status"))

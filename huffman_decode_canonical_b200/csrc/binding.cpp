@@ -47,6 +47,10 @@ bool maybe_tensor(PyObject *o, int &index, const Tensor *&t) {
     t = nullptr;
     return o == Py_None || (t = tensor(o, index)) != nullptr;
 }
+// The status word: None, or an int32 tensor
+bool status_word(PyObject *o, int &index, const Tensor *&t) {
+    return maybe_tensor(o, index, t) && (!t || (t->scalar_type() == ScalarType::Int && t->numel() >= 1));
+}
 bool vector(const Tensor *t, ScalarType type, int64_t n) {
     return t && t->scalar_type() == type && t->dim() == 1 && t->size(0) == n && t->is_contiguous();
 }
@@ -99,7 +103,7 @@ bool scale_of(PyObject *o, int64_t dim, float &scale) {
     double v = 1.0 / std::sqrt(static_cast<double>(dim));
     if (o != Py_None && !number(o, v)) return false;
     scale = static_cast<float>(v);
-    return scale > 0.0f && scale < 3.0e38f;
+    return scale > 0.0f && scale <= 2.0e38f;
 }
 
 // quantize_tokens(x) -> (codes, scale, sum)
@@ -131,7 +135,7 @@ PyObject *matmul_i8(PyObject *, PyObject *const *args, Py_ssize_t n) {
     int index = -1;
     const Tensor *q = tensor(args[0], index), *xs = q ? tensor(args[1], index) : nullptr, *xz = xs ? tensor(args[2], index) : nullptr,
                  *w = xz ? tensor(args[3], index) : nullptr, *ws = nullptr, *wz = nullptr, *status = nullptr;
-    if (!w || !here(index) || !maybe_tensor(args[7], index, status)) Py_RETURN_NONE;
+    if (!w || !here(index) || !status_word(args[7], index, status)) Py_RETURN_NONE;
     if (q->scalar_type() != ScalarType::Char || q->dim() != 2 || q->stride(1) != 1) Py_RETURN_NONE;
     const ScalarType wt = w->scalar_type();
     if ((wt != ScalarType::Byte && wt != ScalarType::Char) || w->dim() != 2 || w->stride(1) != 1) Py_RETURN_NONE;
@@ -165,7 +169,7 @@ PyObject *attention_prompt(PyObject *, PyObject *const *args, Py_ssize_t n) {
     int index = -1;
     const Tensor *q = tensor(args[0], index), *k = q ? tensor(args[1], index) : nullptr, *v = k ? tensor(args[2], index) : nullptr,
                  *cu = v ? tensor(args[3], index) : nullptr, *cu_keys = nullptr, *status = nullptr;
-    if (!cu || !here(index) || !maybe_tensor(args[4], index, cu_keys) || !maybe_tensor(args[6], index, status)) Py_RETURN_NONE;
+    if (!cu || !here(index) || !maybe_tensor(args[4], index, cu_keys) || !status_word(args[6], index, status)) Py_RETURN_NONE;
     const ScalarType type = q->scalar_type();
     if (!half_type(type) || q->dim() != 3 || k->dim() != 3 || cu->dim() != 1 || cu->size(0) < 1) Py_RETURN_NONE;
     const int64_t tokens = q->size(0), heads = q->size(1), dim = q->size(2), keys = k->size(0), kv = k->size(1), batch = cu->size(0) - 1;
@@ -214,7 +218,7 @@ PyObject *kv_append(PyObject *, PyObject *const *args, Py_ssize_t n) {
     if (n != 9 || !c.of(args[0], args[1], args[5], args[7])) Py_RETURN_NONE;
     const Tensor *k = tensor(args[2], c.index), *v = tensor(args[3], c.index), *cu = tensor(args[4], c.index), *lens = tensor(args[6], c.index), *status;
     Rows ks, vs;
-    if (!maybe_tensor(args[8], c.index, status) || !ks.of(k, c.type, c.cache->kv_heads, c.cache->head_dim) ||
+    if (!status_word(args[8], c.index, status) || !ks.of(k, c.type, c.cache->kv_heads, c.cache->head_dim) ||
         !vs.of(v, c.type, c.cache->kv_heads, c.cache->head_dim) || k->size(0) != v->size(0) || !vector(cu, ScalarType::Int, c.batch + 1) ||
         !vector(lens, ScalarType::Int, c.batch))
         Py_RETURN_NONE;
@@ -234,7 +238,7 @@ PyObject *kv_read(PyObject *, PyObject *const *args, Py_ssize_t n) {
     const Tensor *cu = tensor(args[3], c.index), *status;
     int over = 0;
     const long tokens = PyLong_AsLongAndOverflow(args[4], &over);
-    if (over || tokens < 0 || !maybe_tensor(args[6], c.index, status) || !vector(cu, ScalarType::Int, c.batch + 1)) Py_RETURN_NONE;
+    if (over || tokens < 0 || !status_word(args[6], c.index, status) || !vector(cu, ScalarType::Int, c.batch + 1)) Py_RETURN_NONE;
     const int64_t heads = c.cache->kv_heads, dim = c.cache->head_dim;
     Tensor k = make({tokens, heads, dim}, c.type, c.index), v = make({tokens, heads, dim}, c.type, c.index);
     if (f_read(c.cache, k.data_ptr(), heads * dim, dim, v.data_ptr(), heads * dim, dim, tokens, data<int32_t>(cu), data<int32_t>(c.table), c.stride,
@@ -258,7 +262,7 @@ PyObject *kv_attend(PyObject *, PyObject *const *args, Py_ssize_t n) {
     const int64_t dim = c.cache->head_dim, heads = q && q->dim() == 3 ? q->size(1) : 0;
     Rows qs;
     float scale;
-    if (bytes < 1 || !maybe_tensor(args[8], c.index, status) || heads < 1 || heads % c.cache->kv_heads || !qs.of(q, c.type, heads, dim) ||
+    if (bytes < 1 || !status_word(args[8], c.index, status) || heads < 1 || heads % c.cache->kv_heads || !qs.of(q, c.type, heads, dim) ||
         q->size(0) != c.batch || !vector(lens, ScalarType::Int, c.batch) || !scale_of(args[7], dim, scale))
         Py_RETURN_NONE;
     // a workspace of the call's own, from the pool of the stream it runs on: calls never share one

@@ -887,7 +887,7 @@ extern "C" int entro_kv_append(const entro_kv_cache *cache, const void *d_k, int
     if (r != ENTRO_OK) return r;
     if (tokens < 0 || tokens > INT32_MAX || batch < 0 || table_width < 0 || table_stride < table_width) return ENTRO_E_INVAL;
     if (tokens == 0 || batch == 0) return ENTRO_OK;
-    if (!d_k || !d_v || !d_cu || !d_table || !d_lens || !vector_rows(d_k, k_token, k_head) || !vector_rows(d_v, v_token, v_head)) return ENTRO_E_INVAL;
+    if (!d_k || !d_v || !d_cu || (!d_table && table_width > 0) || !d_lens || !vector_rows(d_k, k_token, k_head) || !vector_rows(d_v, v_token, v_head)) return ENTRO_E_INVAL;
     if (!d_slots && batch > cache->slots) return ENTRO_E_INVAL;
     a.in[0] = d_k, a.in[1] = d_v;
     a.in_token[0] = k_token, a.in_token[1] = v_token, a.in_head[0] = k_head, a.in_head[1] = v_head;
@@ -913,7 +913,7 @@ extern "C" int entro_kv_read(const entro_kv_cache *cache, void *d_k, int64_t k_t
     if (r != ENTRO_OK) return r;
     if (tokens < 0 || tokens > INT32_MAX || batch < 0 || table_width < 0 || table_stride < table_width) return ENTRO_E_INVAL;
     if (tokens == 0 || batch == 0) return ENTRO_OK;
-    if (!d_k || !d_v || !d_cu || !d_table || !vector_rows(d_k, k_token, k_head) || !vector_rows(d_v, v_token, v_head)) return ENTRO_E_INVAL;
+    if (!d_k || !d_v || !d_cu || (!d_table && table_width > 0) || !vector_rows(d_k, k_token, k_head) || !vector_rows(d_v, v_token, v_head)) return ENTRO_E_INVAL;
     if (!d_slots && batch > cache->slots) return ENTRO_E_INVAL;
     a.out[0] = d_k, a.out[1] = d_v;
     a.out_token[0] = k_token, a.out_token[1] = v_token, a.out_head[0] = k_head, a.out_head[1] = v_head;
@@ -941,7 +941,7 @@ extern "C" int entro_kv_attend(const entro_kv_cache *cache, const void *d_q, int
     std::memset(&a, 0, sizeof(a));
     int r = make_cache(cache, &a.c);
     if (r != ENTRO_OK) return r;
-    if (batch < 0 || heads < 1 || heads % a.c.kv || table_width < 0 || table_stride < table_width || !(scale > 0.0f) || scale > 3.0e38f)
+    if (batch < 0 || heads < 1 || heads % a.c.kv || table_width < 0 || table_stride < table_width || !(scale > 0.0f) || scale > 2.0e38f)
         return ENTRO_E_INVAL;
     if (batch == 0) return ENTRO_OK;
     if (!d_q || !d_out || !d_lens || !d_work || (!d_table && table_width > 0) || !aligned16(d_work) || !vector_rows(d_q, q_token, q_head) ||

@@ -54,7 +54,9 @@ cudaError_t launch_ex(const void *fn, dim3 grid, unsigned threads, size_t smem, 
         attr[cfg.numAttrs].val.clusterDim.y = attr[cfg.numAttrs].val.clusterDim.z = 1;
         cfg.numAttrs++;
     }
-    return cudaLaunchKernelExC(&cfg, fn, args);
+    const cudaError_t e = cudaLaunchKernelExC(&cfg, fn, args);
+    if (e != cudaSuccess) cudaGetLastError();  // reported by the caller: not left for others to find
+    return e;
 }
 
 int encode_map(CUtensorMap *map, CUtensorMapDataType type, int rank, const void *base, const uint64_t *dims,

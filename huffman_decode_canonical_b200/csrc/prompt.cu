@@ -605,7 +605,7 @@ extern "C" int entro_attention_prompt(int32_t type, int32_t head_dim, const void
                                       const int32_t *d_cu_k, int32_t batch, float scale, void *d_out, int64_t out_token,
                                       int64_t out_head, int32_t *d_status, void *stream) {
     if ((type != ENTRO_BF16 && type != ENTRO_F16) || (head_dim != 64 && head_dim != 96 && head_dim != 128)) return ENTRO_E_INVAL;
-    if (heads < 1 || kv_heads < 1 || heads % kv_heads || tokens < 0 || keys < 0 || batch < 0 || !(scale > 0.0f) || scale > 3.0e38f) return ENTRO_E_INVAL;
+    if (heads < 1 || kv_heads < 1 || heads % kv_heads || tokens < 0 || keys < 0 || batch < 0 || !(scale > 0.0f) || scale > 2.0e38f) return ENTRO_E_INVAL;
     if (tokens > INT32_MAX - 256 || keys > INT32_MAX - 256) return ENTRO_E_LIMIT;
     if (tokens == 0 || batch == 0) return ENTRO_OK;
     if (!d_q || !d_cu_q || !d_out || (keys > 0 && (!d_k || !d_v))) return ENTRO_E_INVAL;

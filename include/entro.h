@@ -227,6 +227,8 @@ ENTRO_API int entro_decode_gemv_group_static(const entro_tensor *const *tensors,
  * so that they may start while the kernel before them on the stream finishes;
  * they touch memory only after it has completed.  Nothing is allocated, on the
  * host heap or on the device, and all calls may be captured into graphs.
+ * Outputs must not overlap inputs.  A call whose waits give up (see
+ * ENTRO_E_TIMEOUT) leaves its outputs incomplete.
  * ------------------------------------------------------------------------ */
 
 /* Element types. */

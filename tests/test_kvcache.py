@@ -170,7 +170,7 @@ def test_refusals_of_the_library():
     for kw in (dict(k=None), dict(ks=4), dict(v=None), dict(tokens=-1), dict(cu=None)):
         assert read(**kw) == entro.E_INVAL, kw
     for kw in (dict(q=None), dict(q=p + 8), dict(qs=12), dict(heads=3), dict(heads=0), dict(lens=None), dict(scale=0.0), dict(scale=-1.0),
-               dict(scale=float("nan")), dict(scale=float("inf")), dict(out=None), dict(work=None), dict(work=p + 4)):
+               dict(scale=float("nan")), dict(scale=float("inf")), dict(scale=3e38), dict(out=None), dict(work=None), dict(work=p + 4)):
         assert attend(**kw) == entro.E_INVAL, kw
     assert append(tokens=0, k=None) == entro.OK and read(batch=0, k=None) == entro.OK and attend(batch=0, q=None) == entro.OK
 
@@ -428,6 +428,47 @@ def test_refusals_on_the_gpu():
                        torch.zeros(9, dtype=torch.int32, device="cuda"))  # more sequences than slots
     with pytest.raises(ValueError, match="gradient"):
         c.cache.attend(q.clone().requires_grad_(), c.table, lens, slots=c.slots)
+    for status in (torch.zeros(1, dtype=torch.int64, device="cuda"), torch.zeros(0, dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32)):
+        for call in (lambda: c.cache.attend(q, c.table, lens, slots=c.slots, status=status), lambda: c.cache.read(c.table, cu, 2, slots=c.slots, status=status),
+                     lambda: c.cache.append(x, x, cu, c.table, lens, slots=c.slots, status=status)):
+            with pytest.raises(ValueError):
+                call()
+
+
+@gpu
+def test_no_pages():
+    """Sequences shorter than a block need no page: a table without columns."""
+    c = Case(2, 2, 64, 16, torch.bfloat16, width=1, seed=13)
+    c.table = torch.zeros((2, 0), dtype=torch.int32, device="cuda")
+    c.append([7, 15])
+    _check_attention(c, 4)
+    got, _ = c.cache.read(c.table, torch.tensor([0, 7, 22], dtype=torch.int32).cuda(), 22, slots=c.slots, status=c.status)
+    assert int(c.status) == 0 and torch.equal(got.cpu(), torch.cat([c.held[0][0], c.held[1][0]]))
+    x = torch.ones(2, 2, 64, dtype=torch.bfloat16, device="cuda")  # the second block fills up: there is no page for it
+    c.cache.append(x, x, torch.tensor([0, 1, 2], dtype=torch.int32).cuda(), c.table, torch.tensor([8, 16], dtype=torch.int32).cuda(), slots=c.slots, status=c.status)
+    assert int(c.status) == entro.E_INVAL
+
+
+@gpu
+def test_given_outputs_and_streams_agree_with_the_usual_call():
+    """The calls that go another way in the binding (an output or a stream given) give the same bits."""
+    c = Case(3, 2, 96, 32, torch.float16, width=5, seed=14)
+    c.append([40, 0, 130])
+    q = torch.randn(3, 8, 96, generator=c.g).to(torch.float16).cuda()
+    lens, cu = c.lens.cuda(), torch.tensor([0, 40, 40, 170], dtype=torch.int32).cuda()
+    want = c.cache.attend(q, c.table, lens, slots=c.slots)
+    assert torch.equal(c.cache.attend(q, c.table, lens, slots=c.slots, out=torch.empty_like(q)), want)
+    assert torch.equal(c.cache.attend(q, c.table, lens, slots=c.slots, stream=torch.cuda.current_stream()), want)
+    k, v = c.cache.read(c.table, cu, 170, slots=c.slots)
+    for a, b in zip((k, v), c.cache.read(c.table, cu, 170, slots=c.slots, out=(torch.empty_like(k), torch.empty_like(v)))):
+        assert torch.equal(a, b)
+    other = entro.KVCache(*(t.clone() for t in (c.cache.k_codes, c.cache.v_codes, c.cache.k_scale, c.cache.v_scale, c.cache.k_tail, c.cache.v_tail)))
+    x, y, one = c.tokens(3).cuda(), c.tokens(3).cuda(), torch.arange(4, dtype=torch.int32, device="cuda")
+    c.cache.append(x, y, one, c.table, lens + 1, slots=c.slots)
+    other.append(x, y, one, c.table, lens + 1, slots=c.slots, stream=torch.cuda.current_stream())
+    for name in ("k_codes", "v_codes", "k_scale", "v_scale", "k_tail", "v_tail"):
+        a, b = getattr(c.cache, name), getattr(other, name)
+        assert torch.equal(torch.nan_to_num(a.float()), torch.nan_to_num(b.float()))
 
 
 @gpu

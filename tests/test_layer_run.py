@@ -122,3 +122,31 @@ def test_layer(bits, fmt, chunk):
             _near(o[b:b + 1], want, mag)
         y = layer["o"][0].decode_gemv(o.view(batch, -1), status=status)
         assert bool(torch.isfinite(y).all()) and int(status) == 0
+
+
+def test_two_streams_at_once():
+    """Each operator on two streams side by side, over and over: the same bits as alone."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(9)
+
+    def normal(*shape):
+        return torch.randn(shape, generator=g, device="cuda").to(torch.bfloat16)
+
+    w = torch.randint(0, 256, (1000, 768), generator=g, device="cuda", dtype=torch.uint8)
+    xs, q, k = [normal(n, 768) for n in (20, 100, 700)], normal(900, 8, 64), normal(900, 2, 64)
+    cu = torch.tensor([0, 300, 900], dtype=torch.int32, device="cuda")
+    cache = entro.KVCache.empty(40, 2, 64, 16, slots=2)
+    table, lens = torch.arange(38, dtype=torch.int32, device="cuda").view(2, 19), torch.tensor([300, 290], dtype=torch.int32, device="cuda")
+    cache.append(k[:590], k[10:600], torch.tensor([0, 300, 590], dtype=torch.int32, device="cuda"), table, lens)
+    work = [lambda x=x: entro.matmul_i8(entro.quantize_tokens(x), w, 0.01, 100) for x in xs]
+    work += [lambda: entro.attention_prompt(q, k, k, cu), lambda: cache.attend(q[:2], table, lens)]
+    want = [f() for f in work]
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in range(2)], []
+    for turn in range(30):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                n = (turn + 2 * i) % len(work)
+                got.append((n, work[n]()))
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, want[n]) for n, y in got)

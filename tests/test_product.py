@@ -265,6 +265,15 @@ def test_product_empty_and_refused():
         entro.matmul_i8(x, w, torch.ones(8, device="cuda", requires_grad=True))
     with torch.no_grad():
         entro.matmul_i8(x, w, torch.ones(8, device="cuda", requires_grad=True))
+    with pytest.raises(ValueError):
+        entro.matmul_i8(x, w, 1.0, status=torch.zeros(1, dtype=torch.int64, device="cuda"))
+    with pytest.raises(entro.EntroError):
+        entro.quantize_tokens(torch.ones(1, 32, dtype=torch.bfloat16, device="cuda").expand(3, 32))
+    # scalars of other kinds, and an output that is given, go another way in the binding: the same bits
+    want = entro.matmul_i8(x, w, 0.5, 3)
+    assert torch.equal(entro.matmul_i8(x, w, np.float32(0.5), np.int64(3)), want)
+    assert torch.equal(entro.matmul_i8(x, w, 0.5, 3, out=torch.empty_like(want)), want)
+    assert torch.equal(entro.matmul_i8(x, w, torch.full((8,), 0.5, device="cuda"), torch.full((8,), 3, dtype=torch.int32, device="cuda")), want)
 
 
 @gpu
