@@ -15,8 +15,8 @@
 // scores take 16384 exponentials, 16 a clock and SM, and 2 x 128 x 128 x D
 // multiply-adds, 4096 a clock), by the exponentials and the instructions around
 // them at 64 and 96.  8192 tokens, 32 heads of 128 over 8: 430 us in a short run (1280
-// TFLOP/s), about 520 in a long one at the power limit; 4096 tokens, 32 heads of 64: 119
-// us (577); 5 prompts of 6011 tokens in all, 32 heads of 96: 97 us (688).  Taking a part of
+// TFLOP/s), about 510 in a long one at the power limit; 4096 tokens, 32 heads of 64: 106
+// to 122 us (563 to 649, from run to run); 5 prompts of 6011 tokens in all, 32 heads of 96: 97 us (688).  Taking a part of
 // the exponentials by a polynomial instead, looking for the maximum only after a weight
 // came out too large, or fetching the next scores beside the exponentials was slower (in
 // an earlier form 463 us -> 489 to 518, 562, and 510).
