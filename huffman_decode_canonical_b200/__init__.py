@@ -512,9 +512,9 @@ def _vector(t: torch.Tensor, name: str, dtype: torch.dtype, n: int, what: str):
         raise ValueError(f"{name} must be a contiguous {dtype} {what} tensor")
 
 
-def _rows(t: torch.Tensor, name: str, dtype: torch.dtype, heads: int, dim: int):
+def _rows(t: torch.Tensor, name: str, dtype: torch.dtype, heads: int, dim: int, written: bool = False):
     """Token and head stride of a [tokens, heads, dim] tensor that the kernels can read in 16-byte pieces (those of a
-    single token or head say nothing and count as 0)."""
+    single token or head say nothing and count as 0); `written`: one whose rows share no elements."""
     shape = t.shape
     if t.dtype is not dtype or len(shape) != 3 or shape[1] != heads or shape[2] != dim:
         raise ValueError(f"{name} must be a {dtype} [tokens, {heads}, {dim}] tensor")
@@ -525,6 +525,9 @@ def _rows(t: torch.Tensor, name: str, dtype: torch.dtype, heads: int, dim: int):
         head = 0
     if channel != 1 or (token | head) & 7 or t.data_ptr() & 15:
         raise ValueError(f"{name} must have adjacent channels, strides that are multiples of 8 and begin on 16 bytes")
+    if written and shape[0] and not any((n <= 1 or s >= dim) and (m <= 1 or r >= (s * (n - 1) if n > 1 else 0) + dim)
+                                        for n, s, m, r in ((heads, head, shape[0], token), (shape[0], token, heads, head))):
+        raise ValueError(f"{name} must not have rows that share elements")
     return token, head
 
 
@@ -563,7 +566,7 @@ def attention_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqle
     elif keys != tokens:
         raise ValueError("without cu_keys, k and v must have q's tokens")
     if out is not None:
-        os_ = _rows(out, "out", dtype, heads, dim)
+        os_ = _rows(out, "out", dtype, heads, dim, written=True)
         if out.shape[0] != tokens:
             raise ValueError("out must have q's shape")
     scale = dim ** -0.5 if scale is None else float(scale)
@@ -614,13 +617,16 @@ class KVCache:
         self._index = k_codes.get_device()
         _check_inputs(self._index, (k_codes, v_codes, k_scale, v_scale, k_tail, v_tail),
                       ("k_codes", "v_codes", "k_scale", "v_scale", "k_tail", "v_tail"))
-        self.k_codes, self.v_codes, self.k_scale, self.v_scale, self.k_tail, self.v_tail = k_codes, v_codes, k_scale, v_scale, k_tail, v_tail
+        self._buffers = k_codes, v_codes, k_scale, v_scale, k_tail, v_tail
         self.pages, self.kv_heads, self.page_tokens, self.head_dim, self.slots, self.dtype = pages, kv, page, dim, slots, dtype
         self._c = _KVCache(k_codes.data_ptr(), v_codes.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), k_tail.data_ptr(),
                            v_tail.data_ptr(), pages, slots, kv, page, dim, _TYPES[dtype])
         self._ref = ctypes.byref(self._c)
         self._address = ctypes.addressof(self._c)
         self._work_bytes = None
+
+    # The buffers are the cache's for good: the library holds their addresses.
+    k_codes, v_codes, k_scale, v_scale, k_tail, v_tail = (property(lambda self, i=i: self._buffers[i]) for i in range(6))
 
     @classmethod
     def empty(cls, pages: int, kv_heads: int, head_dim: int, page_tokens: int = 64, slots: int = 1,
@@ -684,9 +690,11 @@ class KVCache:
         heads, dim = self.kv_heads, self.head_dim
         k, v = (None, None) if out is None else out
         if out is not None:
-            ks, vs = _rows(k, "k", self.dtype, heads, dim), _rows(v, "v", self.dtype, heads, dim)
+            ks, vs = _rows(k, "k", self.dtype, heads, dim, written=True), _rows(v, "v", self.dtype, heads, dim, written=True)
             if k.shape[0] != tokens or v.shape[0] != tokens:
                 raise ValueError(f"out must have {tokens} tokens")
+            if tokens and k.data_ptr() == v.data_ptr():
+                raise ValueError("out's keys and values must be two tensors")
         index = self._index
         _check_inputs(index, (cu_seqlens, page_table, slots, k, v, status), ("cu_seqlens", "page_table", "slots", "k", "v", "status"))
         if stream is not None or index != _current_device():
@@ -719,7 +727,7 @@ class KVCache:
             raise ValueError("q must have a token for each sequence")
         _vector(lens, "lens", torch.int32, batch, "[batch]")
         if out is not None:
-            os_ = _rows(out, "out", self.dtype, heads, dim)
+            os_ = _rows(out, "out", self.dtype, heads, dim, written=True)
             if out.shape[0] != batch:
                 raise ValueError("out must have q's shape")
         scale = dim ** -0.5 if scale is None else float(scale)

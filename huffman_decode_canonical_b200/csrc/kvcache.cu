@@ -914,6 +914,8 @@ extern "C" int entro_kv_read(const entro_kv_cache *cache, void *d_k, int64_t k_t
     if (tokens < 0 || tokens > INT32_MAX || batch < 0 || table_width < 0 || table_stride < table_width) return ENTRO_E_INVAL;
     if (tokens == 0 || batch == 0) return ENTRO_OK;
     if (!d_k || !d_v || !d_cu || (!d_table && table_width > 0) || !vector_rows(d_k, k_token, k_head) || !vector_rows(d_v, v_token, v_head)) return ENTRO_E_INVAL;
+    if (!separate_rows(tokens, a.c.kv, cache->head_dim, k_token, k_head) || !separate_rows(tokens, a.c.kv, cache->head_dim, v_token, v_head))
+        return ENTRO_E_INVAL;
     if (!d_slots && batch > cache->slots) return ENTRO_E_INVAL;
     a.out[0] = d_k, a.out[1] = d_v;
     a.out_token[0] = k_token, a.out_token[1] = v_token, a.out_head[0] = k_head, a.out_head[1] = v_head;
@@ -945,7 +947,7 @@ extern "C" int entro_kv_attend(const entro_kv_cache *cache, const void *d_q, int
         return ENTRO_E_INVAL;
     if (batch == 0) return ENTRO_OK;
     if (!d_q || !d_out || !d_lens || !d_work || (!d_table && table_width > 0) || !aligned16(d_work) || !vector_rows(d_q, q_token, q_head) ||
-        !vector_rows(d_out, out_token, out_head))
+        !vector_rows(d_out, out_token, out_head) || !separate_rows(batch, heads, cache->head_dim, out_token, out_head))
         return ENTRO_E_INVAL;
     if (!d_slots && batch > cache->slots) return ENTRO_E_INVAL;
     r = attend_ctas(&a.ctas);

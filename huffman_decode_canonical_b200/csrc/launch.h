@@ -36,4 +36,16 @@ int encode_map(CUtensorMap *map, CUtensorMapDataType type, int rank, const void 
 
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
+// An output's [tokens][heads] rows of `dim` elements share none: one stride steps over all that the other spans.
+inline bool separate_rows(int64_t tokens, int64_t heads, int64_t dim, int64_t token, int64_t head) {
+    const auto steps = [](int64_t stride, int64_t n, int64_t span) {  // n rows of `span` elements, `stride` apart
+        return n <= 1 || stride >= span;
+    };
+    const auto span = [dim](int64_t stride, int64_t n) {
+        return n <= 1 ? dim : stride > (INT64_MAX - dim) / (n - 1) ? INT64_MAX : (n - 1) * stride + dim;
+    };
+    return (steps(head, heads, dim) && steps(token, tokens, span(head, heads))) ||
+           (steps(token, tokens, dim) && steps(head, heads, span(token, tokens)));
+}
+
 }  // namespace entro

@@ -610,7 +610,8 @@ extern "C" int entro_attention_prompt(int32_t type, int32_t head_dim, const void
     if (tokens == 0 || batch == 0) return ENTRO_OK;
     if (!d_q || !d_cu_q || !d_out || (keys > 0 && (!d_k || !d_v))) return ENTRO_E_INVAL;
     if (!tma_rows(d_q, tokens, heads, q_token, q_head) || !tma_rows(d_k, keys, kv_heads, k_token, k_head) ||
-        !tma_rows(d_v, keys, kv_heads, v_token, v_head) || !aligned16(d_out) || out_token % 8 || out_head % 8)
+        !tma_rows(d_v, keys, kv_heads, v_token, v_head) || !aligned16(d_out) || out_token % 8 || out_head % 8 ||
+        !separate_rows(tokens, heads, head_dim, out_token, out_head))
         return ENTRO_E_INVAL;
     if (!d_cu_k && tokens != keys) return ENTRO_E_INVAL;
     PromptArgs a;

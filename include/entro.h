@@ -277,8 +277,9 @@ ENTRO_API int entro_matmul_i8(const int8_t *d_q, int64_t ldq, const float *d_x_s
 /* Causal attention over packed prompts with grouped heads.  q [tokens][heads]
  * [head_dim], k and v [keys][kv_heads][head_dim] and out like q, of type ENTRO_BF16
  * or ENTRO_F16, head_dim 64, 96 or 128, adjacent channels, strides in elements that
- * are multiples of 8 (of q, k and v above 0), on 16-byte aligned buffers: the parts
- * of one projection's output as they are.  Sequence b's queries are rows d_cu_q[b]
+ * are multiples of 8 (of q, k and v above 0; of out so that no two rows share
+ * elements), on 16-byte aligned buffers: the parts of one projection's output as
+ * they are.  Sequence b's queries are rows d_cu_q[b]
  * to d_cu_q[b+1] (int32 [batch + 1], device), its keys those of d_cu_k (NULL: the
  * same as the queries, tokens == keys).  Its last query sees its last key: query i
  * sees keys j <= i + klen - qlen, so a prompt's next part attends to what came
@@ -323,7 +324,7 @@ typedef struct entro_kv_cache {
  * ones; d_slots int32 [batch], each sequence's tail slot (NULL: slot b for
  * sequence b).  Keys, values, queries and outputs are [tokens or batch][heads]
  * [head_dim] with adjacent channels and any strides (elements) that are multiples
- * of 8, on 16-byte aligned buffers.  Lengths, pages and slots are read on the
+ * of 8, an output's so that no two rows share elements, on 16-byte aligned buffers.  Lengths, pages and slots are read on the
  * device; one that is out of range is reported as ENTRO_E_INVAL in *d_status, and
  * what it names is neither read nor written. */
 

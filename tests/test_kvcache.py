@@ -405,6 +405,31 @@ def test_bad_indices_are_reported():
 
 
 @gpu
+def test_outputs_whose_rows_share_elements_are_refused():
+    c = Case(2, 2, 64, 16, torch.bfloat16, width=3)
+    c.append([5, 6])
+    q, x = torch.zeros(2, 4, 64, dtype=torch.bfloat16, device="cuda"), torch.zeros(11, 2, 64, dtype=torch.bfloat16, device="cuda")
+    cu = torch.tensor([0, 5, 11], dtype=torch.int32).cuda()
+    for out in (q[:1].expand(2, 4, 64), q[:, :1].expand(2, 4, 64)):
+        with pytest.raises(ValueError, match="share"):
+            c.cache.attend(q, c.table, c.lens.cuda(), slots=c.slots, out=out)
+    for out in ((x, x[:1].expand(11, 2, 64)), (x[:, :1].expand(11, 2, 64), x)):
+        with pytest.raises(ValueError, match="share"):
+            c.cache.read(c.table, cu, 11, slots=c.slots, out=out)
+    with pytest.raises(ValueError, match="two tensors"):
+        c.cache.read(c.table, cu, 11, slots=c.slots, out=(x, x))
+
+
+@gpu
+def test_the_buffers_cannot_be_exchanged():
+    # the library holds the addresses of those that it was made of
+    c = Case(1, 2, 64, 16, torch.bfloat16, width=3)
+    for name in ("k_codes", "v_codes", "k_scale", "v_scale", "k_tail", "v_tail"):
+        with pytest.raises(AttributeError):
+            setattr(c.cache, name, getattr(c.cache, name).clone())
+
+
+@gpu
 def test_refusals_on_the_gpu():
     c = Case(2, 2, 64, 16, torch.bfloat16, width=3)
     c.append([5, 6])

@@ -94,6 +94,27 @@ def test_refusals_of_the_binding():
         entro.attention_prompt(q, k, k, cu)
 
 
+@pytest.mark.parametrize("size,stride", [((6, 4, 64), (256, 0, 1)), ((6, 4, 64), (0, 64, 1)), ((6, 4, 64), (192, 64, 1)), ((6, 4, 64), (64, 64, 1)),
+                                         ((6, 4, 64), (56, 448, 1)), ((6, 4, 64), (64, 320, 1))])
+def test_outputs_whose_rows_share_elements_are_refused(size, stride):
+    q, cu = torch.zeros(6, 4, 64, dtype=torch.bfloat16), torch.tensor([0, 6], dtype=torch.int32)
+    out = torch.as_strided(torch.zeros(4096, dtype=torch.bfloat16), size, stride)
+    with pytest.raises(ValueError, match="share"):
+        entro.attention_prompt(q, q, q, cu, out=out)
+    p = 4096
+    assert entro.lib().entro_attention_prompt(entro.BF16, 64, p, 256, 64, 4, 6, p, 256, 64, p, 256, 64, 4, 6, p, None, 1, 0.1, p, stride[0], stride[1],
+                                              None, None) == entro.E_INVAL
+
+
+@pytest.mark.parametrize("stride", [(256, 64, 1), (64, 384, 1), (264, 64, 1), (64, 392, 1), (512, 128, 1)])
+def test_outputs_with_separate_rows_are_taken(stride):
+    # as far as the refusal of CPU tensors
+    q, cu = torch.zeros(6, 4, 64, dtype=torch.bfloat16), torch.tensor([0, 6], dtype=torch.int32)
+    out = torch.zeros(4096, dtype=torch.bfloat16).as_strided((6, 4, 64), stride)
+    with pytest.raises(ValueError, match="CUDA"):
+        entro.attention_prompt(q, q, q, cu, out=out)
+
+
 def test_refusals_of_the_library():
     lib, p = entro.lib(), 4096  # any address: argument errors come before it is used
     good = dict(type=entro.BF16, dim=64, q=p, qt=256, qh=64, heads=4, tokens=8, k=p, kt=128, kh=64, v=p, vt=128, vh=64, kv=2, keys=8, cu=p, cuk=None,
