@@ -22,6 +22,10 @@ uint32_t test_tx_extra();
 // Lets `fn` use all the shared memory a CTA of the device can have (once per kernel and device).
 int allow_smem(const void *fn, int dev);
 
+// How many clusters of `cluster` CTAs the device holds at a time (asked for once per kernel, device and size; the kernel's
+// `threads` and `smem` are always the same).
+int clusters_at_once(const void *fn, int dev, unsigned threads, size_t smem, int cluster, int *clusters);
+
 // A launch with clusters of `cluster` CTAs along x if above 1.  early: it may begin while the kernel
 // before it finishes (its kernel waits for that one before it touches memory).  Only grids whose
 // CTAs are all resident at once start early: CTAs of a larger grid would fill the SMs and wait

@@ -21,6 +21,9 @@
 // came out too large, or fetching the next scores beside the exponentials was slower (in
 // an earlier form 463 us -> 489 to 518, 562, and 510).
 //
+// Few queries over many keys leave most SMs without a block: there a cluster of up
+// to eight CTAs shares the keys of a block (see join_parts).
+//
 // What the mask hides must not count, whatever it holds.  Scores are replaced one
 // by one.  Values of a tile that some row must not see are looked over in shared
 // memory before their MMA: rows past the sequence's keys are zeroed, and where a
@@ -43,6 +46,7 @@ struct PromptArgs {
     int32_t *status;
     int64_t tokens, keys;
     int batch, heads, group;
+    int parts;  // CTAs (a cluster) that share the keys of a block: 1 to 8
     float scale_log2;
     uint32_t tx_extra;
 };
@@ -68,6 +72,7 @@ struct PromptShape {
     static constexpr int kSmem = 1024 + 2 * kQTile + kStages * kTile;
     static constexpr uint32_t kS = 0, kP = 2 * kKeys, kO = 4 * kKeys;  // TMEM columns: S0 S1, P0 P0 P1 P1, O0 O1
     static_assert(kO + 2 * D <= 512 && kStages / 2 < kMarks && kStages >= 4 && kKeys % 32 == 0, "");
+    static_assert(2 * kRows * (D + 2) * 4 <= kSmem - 1024, "");  // a part's outputs and statistics for the join
 };
 
 __device__ __forceinline__ float exp2_fast(float x) {
@@ -133,19 +138,26 @@ __device__ __forceinline__ void row_by_row(const PromptArgs &a, int head, int64_
 // What a CTA works on: 256 queries of a head.
 struct PromptItem {
     int q0, qlen, k0, klen, row0, head;  // head < 0: no more work
+    int offset;                          // query i sees keys up to i + offset
+    int skipped;                         // keys of the sequence in front of k0
 
-    __device__ __forceinline__ int offset() const { return klen - qlen; }  // query i sees keys up to i + offset
     // key tiles of query tile t (0: no rows, or none that sees a key)
     template <int KEYS>
     __device__ __forceinline__ int key_tiles(int t) const {
         const int first = row0 + t * kRows;
         if (first >= qlen) return 0;
-        const int64_t most = static_cast<int64_t>(min(first + kRows, qlen)) + offset();
+        const int64_t most = min(static_cast<int64_t>(min(first + kRows, qlen)) + offset, static_cast<int64_t>(klen));
         return most <= 0 ? 0 : static_cast<int>((most + KEYS - 1) / KEYS);
     }
     // key tiles from here on hold keys that some row must not see
     template <int KEYS>
-    __device__ __forceinline__ int masked_from() const { return offset() + row0 + 1 <= 0 ? 0 : (offset() + row0 + 1) / KEYS; }
+    __device__ __forceinline__ int masked_from() const { return offset + row0 + 1 <= 0 ? 0 : (offset + row0 + 1) / KEYS; }
+    // of the key tiles, part `i` of `of` (its rows see the keys that they saw)
+    template <int KEYS>
+    __device__ __forceinline__ void cut(int i, int of) {
+        const int n = max(key_tiles<KEYS>(0), key_tiles<KEYS>(1)), from = n * i / of * KEYS, to = min(n * (i + 1) / of * KEYS, klen);
+        skipped = from, k0 += from, offset -= from, klen = max(to - from, 0);
+    }
 };
 
 // Block number -> item, by a warp: heads fastest, so that those of a key head meet in L2; of a sequence's blocks the
@@ -177,6 +189,7 @@ __device__ __forceinline__ bool find_item(const PromptArgs &a, int block, Prompt
             const int from = __ffs(here) - 1;
             it.q0 = __shfl_sync(~0u, q0, from), it.qlen = __shfl_sync(~0u, qn, from);
             it.k0 = __shfl_sync(~0u, k0, from), it.klen = __shfl_sync(~0u, kn, from);
+            it.offset = it.klen - it.qlen, it.skipped = 0;
             it.row0 = (__shfl_sync(~0u, sum, from) - 1 - left) * 256;
             return true;
         }
@@ -204,6 +217,97 @@ __device__ __forceinline__ int next_block(uint32_t reply) {  // -1: none is left
         : "memory");
     fence_async_smem();  // read before the next reply is written
     return static_cast<int>(x);
+}
+
+// ---- A block whose keys are shared by a cluster.  Softmax over parts of the keys: with (m_p, l_p, o_p) of part p and
+// m = max m_p, l = sum 2^(c (m_p - m)) l_p and o alike.  Each CTA holds its part's of all 256 rows; they meet in shared
+// memory across the cluster, so there is no workspace and no second launch, and the sums have one order.
+// 256 queries over 32768 keys, 32 heads of 128: 413 us by a CTA a block, 127 by four.
+
+__device__ __forceinline__ void all_warps() { asm volatile("barrier.sync 1, %0;" ::"n"(kPromptThreads) : "memory"); }
+
+// by warps that have no rows (or none that came through): every thread takes part in the barriers
+__device__ __forceinline__ void skip_join() {
+    __syncwarp();
+    all_warps();
+    cluster_sync();
+    cluster_sync();
+}
+
+// By the softmax warps, a row a thread: the parts go to their CTAs' shared memory, where queries, keys and values were
+// (nothing reads those any more when all warps are here), and each CTA finishes a share of the rows.
+template <typename T, int D>
+__device__ __forceinline__ void join_parts(const PromptArgs &a, const PromptItem it, uint32_t base, uint32_t ot, float m, float l, bool any,
+                                        uint32_t special) {
+    const int tid = threadIdx.x, warp = tid / 32;
+    const uint32_t stats = base + 256 * D * 4;
+    __syncwarp();
+    all_warps();
+    tc_fence_after();
+    const int rows = min(256, it.qlen - it.row0);
+#pragma unroll 1
+    for (int x = 0; x < D && warp * 32 < rows; x += 32) {
+        uint32_t o[32];
+        if (any) {
+            tmem_ld32(ot + x, o);
+            tmem_wait_ld<32>(o);
+        } else {
+#pragma unroll
+            for (int y = 0; y < 32; y++) o[y] = 0;
+        }
+        // (eight lanes write 16 bytes each at a time, of rows that begin in the same bank: pieces change places with the row)
+#pragma unroll
+        for (int y = 0; y < 8; y++)
+            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(base + tid * D * 4 + (((x / 4 + y) ^ (tid & 7)) * 16)), "r"(o[4 * y]),
+                         "r"(o[4 * y + 1]), "r"(o[4 * y + 2]), "r"(o[4 * y + 3])
+                         : "memory");
+    }
+    asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(stats + tid * 8), "f"(m), "f"(l) : "memory");
+    __syncwarp();
+    cluster_sync();
+    const int parts = a.parts, share = (rows + parts - 1) / parts, row0 = static_cast<int>(cluster_rank()) * share;
+    const int end = min(row0 + share, rows);
+    uint32_t odd = 0;
+    for (int p = 0; p < parts; p++) {
+        uint32_t x;
+        asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(x) : "r"(map_to(special, p)) : "memory");
+        odd |= x;
+    }
+    if (odd) {
+        for (int r = row0 + warp; r < end; r += 8)
+            row_by_row<T, D>(a, it.head, static_cast<int64_t>(it.q0) + it.row0 + r, it.k0 - it.skipped,
+                             max(it.row0 + r + it.offset + it.skipped + 1, 0));
+    } else {
+        const float c = a.scale_log2;
+        for (int u = tid; u < (end - row0) * (D / 8); u += 256) {
+            const int r = row0 + u / (D / 8), d = u % (D / 8) * 2;  // 8 channels: pieces d and d + 1
+            float2 ml[8];
+            float top = -INFINITY;
+#pragma unroll
+            for (int p = 0; p < 8; p++) ml[p] = p < parts ? load_cluster2(map_to(stats + r * 8, p)) : make_float2(-INFINITY, 0.0f);
+#pragma unroll
+            for (int p = 0; p < 8; p++) top = fmaxf(top, ml[p].x);
+            float sum = 0.0f, o[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int p = 0; p < 8; p++)
+                if (p < parts) {
+                    const uint32_t row = map_to(base + r * D * 4, p);
+                    const float4 x = load_cluster4(row + ((d ^ (r & 7)) * 16)), y = load_cluster4(row + (((d + 1) ^ (r & 7)) * 16));
+                    const float f = ml[p].x == top ? 1.0f : exp2_fast((ml[p].x - top) * c);
+                    sum = fmaf(f, ml[p].y, sum);
+                    o[0] = fmaf(f, x.x, o[0]), o[1] = fmaf(f, x.y, o[1]), o[2] = fmaf(f, x.z, o[2]), o[3] = fmaf(f, x.w, o[3]);
+                    o[4] = fmaf(f, y.x, o[4]), o[5] = fmaf(f, y.y, o[5]), o[6] = fmaf(f, y.z, o[6]), o[7] = fmaf(f, y.w, o[7]);
+                }
+            const float by = sum == 0.0f ? 0.0f : 1.0f / sum;
+            uint32_t h[4];
+#pragma unroll
+            for (int z = 0; z < 4; z++) h[z] = sum == 0.0f ? 0u : Half<T>::pack(o[2 * z] * by, o[2 * z + 1] * by);
+            T *out = static_cast<T *>(a.out) + (static_cast<int64_t>(it.q0) + it.row0 + r) * a.out_token + it.head * a.out_head;
+            *reinterpret_cast<uint4 *>(out + d * 4) = make_uint4(h[0], h[1], h[2], h[3]);
+        }
+    }
+    __syncwarp();
+    cluster_sync();  // the others have read this CTA's part
 }
 
 template <typename T, int D>
@@ -287,11 +391,13 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
         if (warp == 10) {
             // ---- items and copies: queries, then K0 V0 K1 V1 ...
-            int block = blockIdx.x, items_out = 0, queries = 0, i = 0, g = 0, answers = 0;
+            const int rank = blockIdx.x % a.parts;
+            int block = blockIdx.x / a.parts, items_out = 0, queries = 0, i = 0, g = 0, answers = 0;
             PromptItem it;
             while (ok) {
                 const bool is = block >= 0 && find_item(a, block, it);
                 bool soon = false;
+                if (is && a.parts > 1) it.cut<kKeys>(rank, a.parts);
                 if (is || block < 0) {
                     if (block < 0) it.head = -1;
                     if (items_out >= 2) ok = __all_sync(~0u, bar_wait(item_empty + 8 * (items_out % 2), (items_out / 2 - 1) & 1));
@@ -303,7 +409,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                     items_out++;
                     if (block < 0) break;
                     const int n1 = it.key_tiles<kKeys>(1), n = max(it.key_tiles<kKeys>(0), n1), masked_from = it.masked_from<kKeys>();
-                    soon = n <= 4;
+                    soon = n <= 4 && a.parts == 1;
                     if (soon && lane == 0) ask_next(smem_u32(reply), asked);
                     if (n > 0) {
                         if (elect_one()) {
@@ -336,6 +442,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                 // The next item is asked for only now, when all of this one's copies are on their way, unless that is short:
                 // a CTA that asks earlier takes work that another could begin sooner.
                 if (!ok) break;
+                if (a.parts > 1) {  // a block a CTA: all of them are there at once
+                    block = -1;
+                    continue;
+                }
                 if (!soon && lane == 0) ask_next(smem_u32(reply), asked);
                 if (!__all_sync(~0u, bar_wait(asked, answers++ & 1))) ok = false;
                 if (ok) block = next_block(smem_u32(reply));
@@ -445,6 +555,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                 turns += n0 > 0;
             }
         }
+        if (a.parts > 1) skip_join();
     } else {
         // ---- softmax: a row a thread
         asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
@@ -454,9 +565,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         const float c = a.scale_log2;
         PromptItem it;
         int steps = 0, outputs = 0;
+        bool joined = false;
         for (int n_item = 0; ok && take(n_item, it); n_item++) {
             const int nt = it.key_tiles<kKeys>(t), first = it.row0 + t * kRows, row = it.row0 + tid;
-            const int sees = row + it.offset();  // the last key of this row
+            const int sees = row + it.offset;    // the last key of this row
             float m = -INFINITY, l = 0.0f;       // m in units of the raw scores
             for (int j = 0; j < nt; j++) {
                 ok = ok && bar_wait(s_full + 8 * t, (steps + j) & 1);  // (a wait that gave up is the last: no vote a step)
@@ -469,7 +581,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) bar_arrive(s_read + 8 * t);
-                if (j * kKeys + kKeys - 1 > first + it.offset()) {
+                if (j * kKeys + kKeys - 1 > first + it.offset) {
                     const int last = sees - j * kKeys;
 #pragma unroll
                     for (int x = 0; x < kKeys; x++)
@@ -525,6 +637,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                 tc_fence_after();
             }
             if (!ok) break;
+            if (a.parts > 1) {
+                join_parts<T, D>(a, it, base, ot, m, l, nt > 0, smem_u32(special));
+                joined = true;
+                break;
+            }
             if (first < it.qlen) {
                 const float by = l == 0.0f ? 0.0f : 1.0f / l;
                 T *out = static_cast<T *>(a.out) + (static_cast<int64_t>(it.q0) + row) * a.out_token + it.head * a.out_head;
@@ -554,11 +671,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                 // (this tile's values have all been looked over before its output was complete)
                 if (*static_cast<volatile int *>(&special[n_item % 4]) == n_item + 1)
                     for (int r = it.row0 + warp * 32; r < min(it.row0 + warp * 32 + 32, it.qlen); r++)
-                        row_by_row<T, D>(a, it.head, static_cast<int64_t>(it.q0) + r, it.k0, min(max(r + it.offset() + 1, 0), it.klen));
+                        row_by_row<T, D>(a, it.head, static_cast<int64_t>(it.q0) + r, it.k0, max(r + it.offset + 1, 0));
             }
             steps += nt;
             outputs += nt > 0;
         }
+        if (a.parts > 1 && !joined) skip_join();
     }
     if (!ok) failed = 1;
     __syncwarp();
@@ -624,7 +742,7 @@ extern "C" int entro_attention_prompt(int32_t type, int32_t head_dim, const void
     a.tokens = tokens, a.keys = keys, a.batch = batch, a.heads = heads, a.group = heads / kv_heads;
     a.scale_log2 = scale * 1.4426950408889634f;
     a.tx_extra = test_tx_extra();
-    const int64_t blocks = (tokens / 256 + batch) * heads;
+    const int64_t blocks = (tokens + INT64_C(255) * batch) / 256 * heads;  // the most there may be
     if (blocks > INT32_MAX) return ENTRO_E_LIMIT;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -633,6 +751,17 @@ extern "C" int entro_attention_prompt(int32_t type, int32_t head_dim, const void
     const void *fn = type == ENTRO_BF16 ? pick_prompt<__nv_bfloat16>(head_dim, &smem) : pick_prompt<__half>(head_dim, &smem);
     const int keys_of = PromptShape<64>::kKeys;  // (the same for all widths)
     int r = allow_smem(fn, dev);
+    // Few blocks over many keys: as many CTAs share the keys of a block as all find room at once, with four key tiles each
+    // at least on an average sequence.  (40 queries over 4040 keys, 32 heads of 128: 47 us alone, 20 by four; over 1024: 16
+    // and 12.  With clusters that come in two waves, 16 heads by eight: 29, by four 19.  Below 1024 keys there is little to
+    // gain, and results that do not depend on the batch to lose.)
+    a.parts = 1;
+    if (keys / batch >= 1024)
+        for (int parts = static_cast<int>(std::min<int64_t>(keys / batch / 256, 8)); parts > 1 && a.parts == 1 && r == ENTRO_OK; parts--) {
+            int clusters = 0;
+            r = clusters_at_once(fn, dev, kPromptThreads, smem, parts, &clusters);
+            if (blocks <= clusters) a.parts = parts;
+        }
     CUtensorMap q_map, k_map, v_map;
     if (r == ENTRO_OK) r = rows_map(&q_map, type, d_q, tokens, heads, head_dim, q_token, q_head, kRows);
     // (without keys nothing is copied; the maps only have to be valid)
@@ -640,6 +769,6 @@ extern "C" int entro_attention_prompt(int32_t type, int32_t head_dim, const void
     if (r == ENTRO_OK) r = keys ? rows_map(&v_map, type, d_v, keys, kv_heads, head_dim, v_token, v_head, keys_of) : (v_map = q_map, ENTRO_OK);
     if (r != ENTRO_OK) return r;
     void *args[] = {&q_map, &k_map, &v_map, &a};
-    e = launch_ex(fn, dim3(static_cast<unsigned>(blocks)), kPromptThreads, smem, static_cast<cudaStream_t>(stream), 1, false, args);
+    e = launch_ex(fn, dim3(static_cast<unsigned>(blocks * a.parts)), kPromptThreads, smem, static_cast<cudaStream_t>(stream), a.parts, false, args);
     return e == cudaSuccess ? ENTRO_OK : cuda_fail(e, "entro_attention_prompt");
 }

@@ -288,7 +288,9 @@ ENTRO_API int entro_matmul_i8(const int8_t *d_q, int64_t ldq, const float *d_x_s
  * A query that sees no key gets 0; rows of no sequence are left as they are; what
  * the mask hides does not count, infinities and NaN included.  Scores, sums and
  * outputs are taken in fp32, the weights p rounded to `type`; results do not
- * depend on the other sequences of the batch.  Offsets out of range are reported
+ * depend on the other sequences of the batch, unless the whole call's few queries
+ * leave SMs free to share keys (1024 keys a sequence on average or more): then the
+ * batch decides where sums are cut.  Offsets out of range are reported
  * as ENTRO_E_INVAL in *d_status and their sequence is skipped. */
 ENTRO_API int entro_attention_prompt(int32_t type, int32_t head_dim, const void *d_q, int64_t q_token, int64_t q_head,
                                      int32_t heads, int64_t tokens, const void *d_k, int64_t k_token, int64_t k_head,

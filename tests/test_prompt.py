@@ -226,6 +226,70 @@ def test_rows_of_no_sequence():
     _check(q[:400], k[:400], v[:400], cu, got=got[:400])
 
 
+# Few queries over many keys: a cluster of CTAs shares a block's keys (from 1024 keys a sequence on, up to eight CTAs).
+@gpu
+@pytest.mark.parametrize("dim", [64, 96, 128])
+@pytest.mark.parametrize("queries,keys", [([1], [1024]), ([1], [4096]), ([2], [4097]), ([40], [5003]), ([128], [2048]), ([129], [3001]), ([300], [4500]),
+                                          ([256], [4160]), ([130, 0, 7], [2100, 5000, 3000]), ([1500], [1500]), ([1300], [1200]), ([3, 5], [8, 9000])])
+def test_keys_shared_by_a_cluster(queries, keys, dim):
+    g = _gen(21, len(queries), keys[0], dim)
+    q, k, v = _inputs(g, sum(queries), sum(keys), 2, 1, dim, torch.float16 if sum(queries) % 2 else torch.bfloat16)
+    got = _check(q, k, v, _cu(queries), _cu(keys))
+    for _ in range(3):
+        assert torch.equal(got, entro.attention_prompt(q.cuda(), k.cuda(), v.cuda(), _cu(queries).cuda(), _cu(keys).cuda()))
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_sharp_scores_in_shared_keys(dtype):
+    # the largest score lies in one part, by far; each part in turn
+    g = _gen(22)
+    q, k, v = _inputs(g, 70, 4200, 4, 2, 128, dtype)
+    for at in (0, 600, 1100, 2047, 2048, 3000, 3600, 4100):
+        w = k.clone()
+        w[at] = 8 * q[35, 0]
+        _check(q, w, v, _cu([70]), _cu([4200]))
+
+
+@gpu
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf")])
+def test_hidden_values_in_shared_keys(value):
+    g = _gen(23)
+    q, k, v = _inputs(g, 300, 4400, 2, 1, 96, torch.bfloat16)
+    plain = _check(q, k, v, _cu([300]), _cu([4400]))
+    for at in (4100, 4101, 4228, 4399):
+        w = v.clone()
+        w[at, 0, 3] = value
+        got = _check(q, k, w, _cu([300]), _cu([4400]))
+        assert bool(torch.isfinite(got[:at - 4100]).all()) and bool(torch.isfinite(got[:, :, 4:]).all())
+        w = k.clone()
+        w[at, 0, 3] = value
+        got = entro.attention_prompt(q.cuda(), w.cuda(), v.cuda(), _cu([300]).cuda(), _cu([4400]).cuda())
+        assert torch.equal(got[:at - 4100], plain[:at - 4100])
+    # bad offsets: reported, and the other sequence's rows are right
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = torch.full_like(q, 7).cuda()
+    cu, cu_k = torch.tensor([0, 100, 301], dtype=torch.int32), torch.tensor([0, 4100, 4400], dtype=torch.int32)
+    entro.attention_prompt(q.cuda(), k.cuda(), v.cuda(), cu.cuda(), cu_k.cuda(), out=out, status=status)
+    assert int(status) == entro.E_INVAL and bool((out[100:] == 7).all())
+    _check(q[:100], k[:4100], v[:4100], _cu([100]), _cu([4100]), got=out[:100])
+
+
+@gpu
+def test_wait_gives_up_with_shared_keys():
+    g = _gen(24)
+    q, k, v = _inputs(g, 50, 5000, 2, 1, 64, torch.bfloat16)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    entro.test_stall_tables(16)
+    try:
+        entro.attention_prompt(q.cuda(), k.cuda(), v.cuda(), _cu([50]).cuda(), _cu([5000]).cuda(), status=status)
+        torch.cuda.synchronize()
+    finally:
+        entro.test_stall_tables(0)
+    assert int(status) == entro.E_TIMEOUT
+    _check(q, k, v, _cu([50]), _cu([5000]))
+
+
 @gpu
 def test_batch_does_not_matter():
     g = _gen(11)
