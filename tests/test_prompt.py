@@ -4,6 +4,10 @@ Bound for an output o = sum p v: the weights are rounded to the type (half a ste
 32-bit sums of head_dim products, off by a few 2^-23 of the sum of the products' magnitudes (16 x 2^-23: a rounding per MMA
 and the scale's), which moves a weight by that much of itself, in numerator and sum; the 32-bit sums over the keys take a
 rounding per 16 keys and 64 more; the rest is below 2^-18 of sum p |v|; the output is rounded by h |o|."""
+import pathlib
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -273,6 +277,42 @@ def test_hidden_values_in_shared_keys(value):
     entro.attention_prompt(q.cuda(), k.cuda(), v.cuda(), cu.cuda(), cu_k.cuda(), out=out, status=status)
     assert int(status) == entro.E_INVAL and bool((out[100:] == 7).all())
     _check(q[:100], k[:4100], v[:4100], _cu([100]), _cu([4100]), got=out[:100])
+
+
+_FIRST_CALL = """
+import torch, huffman_decode_canonical_b200 as entro
+g = torch.Generator(device="cuda").manual_seed(1)
+q, k, v = (torch.randn(t, h, 64, generator=g, device="cuda").half() for t, h in ((40, 4), (5000, 2), (5000, 2)))
+cu, cu_k = torch.tensor([0, 40], dtype=torch.int32, device="cuda"), torch.tensor([0, 5000], dtype=torch.int32, device="cuda")
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    y = entro.attention_prompt(q, k, v, cu, cu_k)
+graph.replay()
+first = y.clone()
+cu_k[1] = 3000  # the table of a replay is the one of its time
+graph.replay()
+torch.cuda.synchronize()
+assert torch.equal(first, entro.attention_prompt(q, k, v, cu, torch.tensor([0, 5000], dtype=torch.int32, device="cuda")))
+seen = entro.attention_prompt(q, k[:3000], v[:3000], cu, cu_k).double()
+assert (y.double() - seen).abs().max() <= 2.0 ** -9
+a, b, outs = torch.cuda.Stream(), torch.cuda.Stream(), []
+torch.cuda.synchronize()
+for _ in range(20):
+    for s in (a, b):
+        outs.append(entro.attention_prompt(q, k, v, cu, cu_k, stream=s))
+torch.cuda.synchronize()
+assert all(torch.equal(o, y) for o in outs)
+print("good")
+"""
+
+
+@gpu
+def test_shared_keys_captured_first_and_on_two_streams():
+    """A process whose first call is captured; then two streams at once.  Between the two cuts of the same sums: each side's
+    weights are rounded to fp16 (2^-11 of sum p |v|, which is near 0.8 and below 1) and its output (below 2^-2: 2^-14);
+    2 (2^-11 + 2^-14) is below 2^-9, with room for the 32-bit sums."""
+    done = subprocess.run([sys.executable, "-c", _FIRST_CALL], cwd=pathlib.Path(__file__).resolve().parents[1], capture_output=True, text=True, timeout=120)
+    assert done.returncode == 0 and done.stdout.strip() == "good", done.stderr[-2000:]
 
 
 @gpu
