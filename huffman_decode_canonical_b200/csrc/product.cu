@@ -31,16 +31,14 @@ struct QuantArgs {
     int64_t tokens, cols, ldx, ldq;
 };
 
-constexpr int kQuantThreads = 256;
-
 // One CTA a token.  The row stays in registers between its two uses (VECS
 // 16-byte loads a thread; 0: rows too long or too unaligned for that, read twice
-// element by element).  Bound by memory, 3 bytes an element: 8192 x 14336 in 75 us,
-// 4.7 TB/s.
-template <typename T, int VECS>
-__global__ void __launch_bounds__(kQuantThreads) quantize_kernel(const QuantArgs a) {
-    __shared__ uint32_t red_max[kQuantThreads / 32];
-    __shared__ int red_sum[kQuantThreads / 32];
+// element by element).  Bound by memory, 3 bytes an element: 8192 x 14336 in 65 to
+// 70 us, 5.2 TB/s; 500 x 28672 in 11 us (read twice: 29).
+template <typename T, int THREADS, int VECS>
+__global__ void __launch_bounds__(THREADS) quantize_kernel(const QuantArgs a) {
+    __shared__ uint32_t red_max[THREADS / 32];
+    __shared__ int red_sum[THREADS / 32];
     dependents_may_launch();
     const int tid = threadIdx.x;
     const int64_t t = blockIdx.x;
@@ -50,7 +48,7 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_kernel(const QuantArgs
     if (VECS) {
 #pragma unroll
         for (int i = 0; i < VECS; i++) {
-            const int64_t k = (static_cast<int64_t>(i) * kQuantThreads + tid) * 8;
+            const int64_t k = (static_cast<int64_t>(i) * THREADS + tid) * 8;
             v[i] = make_uint4(0, 0, 0, 0);
             if (k + 8 <= a.cols) {
                 v[i] = __ldg(reinterpret_cast<const uint4 *>(row + k));
@@ -63,20 +61,20 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_kernel(const QuantArgs
                                      __vmaxu2(v[i].z & 0x7FFF7FFFu, v[i].w & 0x7FFF7FFFu)));
         }
     } else {
-        for (int64_t k = tid; k < a.cols; k += kQuantThreads) m = max(m, static_cast<uint32_t>(row[k] & 0x7FFF));
+        for (int64_t k = tid; k < a.cols; k += THREADS) m = max(m, static_cast<uint32_t>(row[k] & 0x7FFF));
     }
     m = max(m & 0xFFFF, m >> 16);
     m = __reduce_max_sync(~0u, m);
     if (tid % 32 == 0) red_max[tid / 32] = m;
     __syncthreads();
     m = 0;
-    for (int w = 0; w < kQuantThreads / 32; w++) m = max(m, red_max[w]);
+    for (int w = 0; w < THREADS / 32; w++) m = max(m, red_max[w]);
     const BlockCode<T> code(m);
     int sum = 0;
     if (VECS) {
 #pragma unroll
         for (int i = 0; i < VECS; i++) {
-            const int64_t k = (static_cast<int64_t>(i) * kQuantThreads + tid) * 8;
+            const int64_t k = (static_cast<int64_t>(i) * THREADS + tid) * 8;
             if (k >= a.cols) break;
             const uint2 o = code.eight(v[i]);
             sum = __dp4a(static_cast<int>(o.x), 0x01010101, __dp4a(static_cast<int>(o.y), 0x01010101, sum));
@@ -84,7 +82,7 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_kernel(const QuantArgs
             *reinterpret_cast<uint2 *>(a.q + t * a.ldq + k) = o;
         }
     } else {
-        for (int64_t k = tid; k < a.cols; k += kQuantThreads) {
+        for (int64_t k = tid; k < a.cols; k += THREADS) {
             const int c = code.one(Half<T>::widen(row[k]).x);
             a.q[t * a.ldq + k] = static_cast<int8_t>(c);
             sum += c;
@@ -95,7 +93,7 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_kernel(const QuantArgs
     __syncthreads();
     if (tid == 0) {
         sum = 0;
-        for (int w = 0; w < kQuantThreads / 32; w++) sum += red_sum[w];
+        for (int w = 0; w < THREADS / 32; w++) sum += red_sum[w];
         a.sum[t] = sum;
         a.scale[t] = code.scale();
     }
@@ -541,15 +539,16 @@ static double narrow_cycles(int64_t row_tiles, int split, int sms, int chunks, i
     return static_cast<double>((ctas + sms - 1) / sms) * ((chunks + split - 1) / split) * step + 9000 + (split > 1 ? 60.0 * bn : 0.0);
 }
 
+// 256 threads of up to four 16-byte loads; from 8192 columns on 512 (14336: 65 to 70 us, by 256 of eight loads 74 to 81).
 template <typename T>
-static const void *pick_quantize(int vecs) {
-    switch (vecs) {
-        case 1: return reinterpret_cast<const void *>(quantize_kernel<T, 1>);
-        case 2: return reinterpret_cast<const void *>(quantize_kernel<T, 2>);
-        case 4: return reinterpret_cast<const void *>(quantize_kernel<T, 4>);
-        case 8: return reinterpret_cast<const void *>(quantize_kernel<T, 8>);
-        default: return reinterpret_cast<const void *>(quantize_kernel<T, 0>);
-    }
+static const void *pick_quantize(int64_t cols, bool whole, unsigned *threads) {
+    *threads = whole && cols > 8192 && cols <= 32768 ? 512 : 256;
+    return !whole || cols > 32768 ? reinterpret_cast<const void *>(quantize_kernel<T, 256, 0>)
+           : cols <= 2048         ? reinterpret_cast<const void *>(quantize_kernel<T, 256, 1>)
+           : cols <= 4096         ? reinterpret_cast<const void *>(quantize_kernel<T, 256, 2>)
+           : cols <= 8192         ? reinterpret_cast<const void *>(quantize_kernel<T, 256, 4>)
+           : cols <= 16384        ? reinterpret_cast<const void *>(quantize_kernel<T, 512, 4>)
+                                  : reinterpret_cast<const void *>(quantize_kernel<T, 512, 8>);
 }
 
 }  // namespace entro
@@ -562,15 +561,12 @@ extern "C" int entro_quantize_tokens(const void *d_x, int32_t type, int64_t toke
     if (tokens > ENTRO_PRODUCT_MAX_TOKENS || cols > ENTRO_PRODUCT_MAX_COLS) return ENTRO_E_LIMIT;
     if (tokens == 0) return ENTRO_OK;
     if (!d_x || !d_q || !d_scale || !d_sum || ldq % 16 || !aligned16(d_q) || (reinterpret_cast<uintptr_t>(d_x) & 1)) return ENTRO_E_INVAL;
-    int vecs = 0;
-    if (aligned16(d_x) && ldx % 8 == 0) {
-        const int64_t need = (cols + kQuantThreads * 8 - 1) / (kQuantThreads * 8);
-        vecs = need <= 1 ? 1 : need <= 2 ? 2 : need <= 4 ? 4 : need <= 8 ? 8 : 0;
-    }
     QuantArgs a{static_cast<const uint16_t *>(d_x), d_q, d_scale, d_sum, tokens, cols, ldx, ldq};
-    const void *fn = type == ENTRO_BF16 ? pick_quantize<__nv_bfloat16>(vecs) : pick_quantize<__half>(vecs);
+    const bool whole = aligned16(d_x) && ldx % 8 == 0;  // rows in 16-byte pieces
+    unsigned threads;
+    const void *fn = type == ENTRO_BF16 ? pick_quantize<__nv_bfloat16>(cols, whole, &threads) : pick_quantize<__half>(cols, whole, &threads);
     void *args[] = {&a};
-    cudaError_t e = launch_ex(fn, dim3(static_cast<unsigned>(tokens)), kQuantThreads, 0, static_cast<cudaStream_t>(stream), 1, false, args);
+    cudaError_t e = launch_ex(fn, dim3(static_cast<unsigned>(tokens)), threads, 0, static_cast<cudaStream_t>(stream), 1, false, args);
     return e == cudaSuccess ? ENTRO_OK : cuda_fail(e, "entro_quantize_tokens");
 }
 

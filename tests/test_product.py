@@ -142,6 +142,22 @@ def test_quantize_exact(dtype, tokens, cols):
 
 @gpu
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("cols", [8192, 8193, 12001, 16385, 28672, 32768, 32769, 65536])
+def test_quantize_long_rows(dtype, cols):
+    for tokens in (1, 5):
+        x = _tokens(_rng(tokens, cols, 1), tokens, cols, dtype)
+        x[0, -1] = 2 * x[0].abs().max()  # the last column decides
+        got = entro.quantize_tokens(x.cuda())
+        q, scale = _codes64(x)
+        assert torch.equal(got.codes.cpu().double(), q) and torch.equal(got.sum.cpu().double(), q.sum(1))
+        assert torch.equal(got.scale.cpu(), x.float().abs().amax(1) / 127)
+    y = torch.zeros(3, cols + 1, dtype=dtype)  # rows that do not begin on 16 bytes
+    y[:, 1:] = _tokens(_rng(3, cols, 2), 3, cols, dtype)
+    assert torch.equal(entro.quantize_tokens(y.cuda()[:, 1:]).codes.cpu().double(), _codes64(y[:, 1:])[0])
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
 def test_quantize_every_ratio(dtype):
     """Each significand of x against each of the largest value: every quotient that can tie."""
     bits = 128 if dtype == torch.bfloat16 else 1024
