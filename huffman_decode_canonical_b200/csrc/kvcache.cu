@@ -176,12 +176,22 @@ struct ReadArgs {
     int batch, table_width;
 };
 
+// Where a sequence's tokens lie among the packed ones; false for offsets that the call does not allow.  (Compared before
+// they are subtracted: the difference of two 32-bit offsets may pass 32 bits.)
+__device__ __forceinline__ bool packed_range(const ReadArgs &a, int b, int &begin, int &end) {
+    begin = a.cu[b], end = a.cu[b + 1];
+    return begin >= 0 && begin <= end && end <= a.tokens;
+}
+
 // Cached tokens back to 16 bits: code times scale in 32 bits, rounded once.  A
 // warp takes a token at a time; bound by memory: 36000 tokens of 8 x 128 in 46 us, 4.8 TB/s.
 template <typename T, int D>
 __global__ void __launch_bounds__(256) read_kernel(const ReadArgs a) {
     const int lane = threadIdx.x % 32, P = 1 << a.c.log_page;
     const int64_t t = blockIdx.x * 8LL + threadIdx.x / 32;
+    int begin, end;
+    for (int64_t b = blockIdx.x * 256LL + threadIdx.x; b < a.batch; b += gridDim.x * 256LL)
+        if (!packed_range(a, static_cast<int>(b), begin, end)) set_status(a.status, ENTRO_E_INVAL);
     if (t >= a.tokens) return;
     // the last sequence that begins at or before t
     int lo = 0, hi = a.batch;
@@ -190,8 +200,8 @@ __global__ void __launch_bounds__(256) read_kernel(const ReadArgs a) {
         if (a.cu[mid] <= t) lo = mid;
         else hi = mid;
     }
-    const int b = lo, begin = a.cu[b], end = a.cu[b + 1];
-    if (t < begin || t >= end) return;  // a token of no sequence: left as it is
+    const int b = lo;
+    if (!packed_range(a, b, begin, end) || t < begin || t >= end) return;  // a token of no sequence: left as it is
     const int pos = static_cast<int>(t) - begin, block = pos >> a.c.log_page;
     const int slot = a.slot_of ? a.slot_of[b] : b;
     const bool open = block == (end - begin) >> a.c.log_page;
