@@ -46,15 +46,17 @@ constexpr int kAppendThreads = 128;
 // The sequence's new tokens [begin, begin + n) and its first new position; n = 0
 // for what the arguments do not allow (reported once).
 __device__ __forceinline__ int new_tokens(const AppendArgs &a, int b, int &begin, int &start) {
-    begin = a.cu[b];
-    const int end = a.cu[b + 1], len = a.lens[b], n = end - begin;
-    start = len - n;
+    begin = a.cu[b], start = 0;
+    const int end = a.cu[b + 1], len = a.lens[b];
     const int slot = a.slot_of ? a.slot_of[b] : b;
-    if (begin < 0 || n < 0 || end > a.tokens || start < 0 || slot < 0 || slot >= a.c.slots ||
-        (n > 0 && len >> a.c.log_page > a.table_width)) {
+    // (compared before they are subtracted: differences of these numbers may pass 32 bits)
+    const bool ok = begin >= 0 && begin <= end && end <= a.tokens && len >= 0 && end - begin <= len && slot >= 0 && slot < a.c.slots;
+    const int n = ok ? end - begin : 0;
+    if (!ok || (n > 0 && len >> a.c.log_page > a.table_width)) {
         set_status(a.status, ENTRO_E_INVAL);
         return 0;
     }
+    start = len - n;
     return n;
 }
 

@@ -47,3 +47,22 @@ def test_read(cu, right):
             assert torch.equal(got[cu[b]:cu[b + 1]], w[at[b]:at[b] + n[b]])
             left[cu[b]:cu[b + 1]] = False
         assert bool((got.cpu()[left] == 7).all())
+
+
+@gpu
+@pytest.mark.parametrize("cu,lens", [((0, 3, 5), (LOW, 22)), ((0, 3, 5), (LOW + 2, 22)), ((0, 3, 5), (2, 22)), ((1, LOW, 2), (43, 22)), ((1, LOW, 2), (HIGH, HIGH)),
+                                     ((LOW, 3, 5), (43, 22)), ((0, HIGH, 5), (HIGH, 22)), ((0, 3, 5), (HIGH, 22)), ((0, 6, 5), (46, 22))])
+def test_append(cu, lens):
+    cache, table, slots, _ = _cache()
+    held = [t.clone() for t in cache._buffers]
+    status, x = _status(), torch.ones(5, 2, 64, dtype=torch.bfloat16, device="cuda")
+    cache.append(x, x, _ints(*cu), table, _ints(*lens), slots=slots, status=status)
+    assert int(status) == entro.E_INVAL
+    second = cu[1] == 3 and lens[1] == 22  # sequence 1's arguments are right: two more tokens after its 20, in slot 0
+    for i, (now, was) in enumerate(zip(cache._buffers, held)):
+        if i >= 4 and second:  # the tails
+            assert bool((now[0, :, 4:6] == 1).all())
+            now, was = now.clone(), was.clone()
+            now[0, :, 4:6] = was[0, :, 4:6] = 0
+        # (the rest may hold NaN: compared as whole numbers)
+        assert torch.equal(now.view(torch.int8), was.view(torch.int8))
