@@ -170,13 +170,13 @@ __device__ __forceinline__ bool find_item(const PromptArgs &a, int block, Prompt
         const int b = b0 + lane;
         int q0 = 0, qn = 0, k0 = 0, kn = 0;
         if (b < a.batch) {
-            q0 = a.cu_q[b], qn = a.cu_q[b + 1] - q0;
-            k0 = a.cu_k[b], kn = a.cu_k[b + 1] - k0;
-            if (q0 < 0 || qn < 0 || static_cast<int64_t>(q0) + qn > a.tokens || k0 < 0 || kn < 0 ||
-                static_cast<int64_t>(k0) + kn > a.keys) {
+            q0 = a.cu_q[b], k0 = a.cu_k[b];
+            const int q1 = a.cu_q[b + 1], k1 = a.cu_k[b + 1];
+            // (compared before they are subtracted: differences of offsets may pass 32 bits)
+            if (q0 < 0 || q0 > q1 || q1 > a.tokens || k0 < 0 || k0 > k1 || k1 > a.keys)
                 set_status(a.status, ENTRO_E_INVAL);
-                qn = 0;
-            }
+            else
+                qn = q1 - q0, kn = k1 - k0;
         }
         const int blocks = qn / 256 + (qn % 256 != 0);
         int sum = blocks;

@@ -66,3 +66,22 @@ def test_append(cu, lens):
             now[0, :, 4:6] = was[0, :, 4:6] = 0
         # (the rest may hold NaN: compared as whole numbers)
         assert torch.equal(now.view(torch.int8), was.view(torch.int8))
+
+
+@gpu
+@pytest.mark.parametrize("cu,right", [((1, LOW, 100), []), ((40, LOW + 3, 100), []), ((LOW, 40, 100), [1]), ((0, 40, LOW), [0]), ((0, HIGH, LOW), []), ((LOW, LOW, LOW), [])])
+@pytest.mark.parametrize("of", ["queries", "keys", "both"])
+def test_prompt(cu, right, of):
+    g = torch.Generator().manual_seed(4)
+    q, k = (torch.randn(100, h, 64, generator=g).to(torch.bfloat16).cuda() for h in (4, 2))
+    good, bad = _ints(0, 40, 100), _ints(*cu)
+    want = entro.attention_prompt(q, k, k, good)
+    out, status = torch.full_like(q, 7.0), _status()
+    entro.attention_prompt(q, k, k, bad if of != "keys" else good, None if of == "both" else bad if of == "keys" else good, out=out, status=status)
+    assert int(status) == entro.E_INVAL
+    left = torch.ones(100, dtype=torch.bool)
+    for b in right:
+        at = slice(40 * b, 40 + 60 * b)
+        assert torch.equal(out[at], want[at])
+        left[at] = False
+    assert bool((out.cpu()[left] == 7).all())
