@@ -348,6 +348,11 @@ __device__ __forceinline__ void mma16816(float *c, const uint32_t *a, uint32_t b
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ void mma16816_bf16(float *c, const uint32_t *a, uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
     uint32_t r;
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
@@ -452,8 +457,8 @@ struct Running {
     }
 
     // s: scores in units of log2 (tokens gid and gid + 8 of heads 2 tig, 2 tig + 1), -inf
-    // where there is no token; on return the weights as the P^T operand.
-    __device__ __forceinline__ void weights(const float *s, uint32_t &p0, uint32_t &p1) {
+    // where there is no token; on return their weights.
+    __device__ __forceinline__ void weights(float *s) {
         const float t0 = m[0] + kLazy, t1 = m[1] + kLazy;
         if (__any_sync(~0u, s[0] > t0 || s[2] > t0 || s[1] > t1 || s[3] > t1)) {
             float n0 = fmaxf(s[0], s[2]), n1 = fmaxf(s[1], s[3]);
@@ -474,12 +479,17 @@ struct Running {
         }
         // no score so far: any reference does
         const float r0 = (m[0] == -INFINITY ? 0.0f : m[0]) - kBias, r1 = (m[1] == -INFINITY ? 0.0f : m[1]) - kBias;
-        const float e0 = ex2(s[0] - r0), e1 = ex2(s[1] - r1), e2 = ex2(s[2] - r0), e3 = ex2(s[3] - r1);
-        l[0] += e0 + e2;
-        l[1] += e1 + e3;
-        p0 = transpose8x8(Half<__half>::pack(e0, e1));
-        p1 = transpose8x8(Half<__half>::pack(e2, e3));
+        s[0] = ex2(s[0] - r0), s[1] = ex2(s[1] - r1), s[2] = ex2(s[2] - r0), s[3] = ex2(s[3] - r1);
+        l[0] += s[0] + s[2];
+        l[1] += s[1] + s[3];
     }
+};
+
+// Weights as the P^T operand in fp16 (2^-11 of a weight at most).
+struct Weights16 {
+    uint32_t p0, p1;
+    __device__ __forceinline__ explicit Weights16(const float *e)
+        : p0(transpose8x8(Half<__half>::pack(e[0], e[1]))), p1(transpose8x8(Half<__half>::pack(e[2], e[3]))) {}
 };
 
 // One pass over the cache.  A CTA's share of all tiles is one row of tiles, cut
@@ -501,6 +511,7 @@ constexpr int attend_smem() {
 template <typename T, int D>
 __global__ void __launch_bounds__(kAttendThreads, 4) attend_kernel(const AttendArgs a) {
     using Layout = StepLayout<D>;
+    constexpr bool kBf16 = Half<T>::kExp != 0x7C007C00u;
     constexpr int kK = D / 4, kV = D / 8;  // bytes of a token's codes that a thread reads: keys (2 tokens), values (4)
     constexpr int kKLoad = kK % 16 == 0 ? 16 : 8, kVLoad = kV % 16 == 0 ? 16 : kV % 8 == 0 ? 8 : 4;
     extern __shared__ __align__(16) uint8_t smem[];  // the warps' steps, then their outputs
@@ -537,20 +548,18 @@ __global__ void __launch_bounds__(kAttendThreads, 4) attend_kernel(const AttendA
         const int full = len >> a.c.log_page << a.c.log_page;  // tokens in coded blocks
         const int32_t *pages = a.table + seq * a.table_stride;
 
-        // Steps of 16 tokens, kSteps - 1 of them on their way.  A step that is not of coded blocks (the tail's, past the
-        // end, on a page that does not exist) copies nothing; bit x of `coded` says of the step in place x whether it did.
+        // Steps of 16 tokens, kSteps - 1 of them on their way; this warp's tiles up to `coded_end` are of coded blocks.  A
+        // step on a page that does not exist copies nothing; bit x of `coded` says of the step in place x whether it did.
+        const int coded_end = min(t1, (full - warp * 16 + kTile - 1) / kTile);
         uint32_t coded = 0;
         int place = 0;  // of the next step to be sent
-        auto page_of = [&](int tile) {
-            const int tok = tile * kTile + warp * 16;
-            return tile < t1 && tok < full ? __ldg(pages + (tok >> a.c.log_page)) : -1;
-        };
+        auto page_of = [&](int tile) { return tile < coded_end ? __ldg(pages + ((tile * kTile + warp * 16) >> a.c.log_page)) : -1; };
         int page = page_of(t0);
         auto send = [&](int tile) {
             const int tok = tile * kTile + warp * 16, p = page;
             page = page_of(tile + 1);
             coded &= ~(1u << place);
-            if (tile < t1 && tok < full) {
+            if (tile < coded_end) {
                 if (p >= 0 && p < a.c.pages) {
                     const int64_t block = static_cast<int64_t>(p) * a.c.kv + h, from = (block * P + (tok & (P - 1))) * D;
                     const uint32_t to = steps + place * Layout::kBytes;
@@ -574,10 +583,10 @@ __global__ void __launch_bounds__(kAttendThreads, 4) attend_kernel(const AttendA
         // Q as the second operand: head gid, channels tig D / 4 + 4 s + 0 .. 3 in step s
         uint32_t q[D / 16][2];
         float mine = 0.0f;
+        auto q_row = [&](int head) { return static_cast<const T *>(a.q) + seq * a.q_token + (head0 + min(head, heads - 1)) * a.q_head; };
         {
-            const T *row = static_cast<const T *>(a.q) + seq * a.q_token + (head0 + min(gid, heads - 1)) * a.q_head + tig * kK;
             uint32_t raw[D / 8], top = 0;
-            load_bytes<D / 2>(raw, row);
+            load_bytes<D / 2>(raw, q_row(gid) + tig * kK);
 #pragma unroll
             for (int i = 0; i < D / 8; i++) top = __vmaxu2(top, raw[i] & 0x7FFF7FFFu);
             top = max(top & 0xFFFF, top >> 16);
@@ -592,124 +601,137 @@ __global__ void __launch_bounds__(kAttendThreads, 4) attend_kernel(const AttendA
 
         Running<D> r;
         r.clear();
-        // a thread's keys are tokens gid and gid + 8, its values tokens 2 tig, 2 tig + 1 and those + 8
-        int here = 0;
-        for (int tile = t0; tile < t1; tile++) {
+        // Steps of coded tokens: a thread's keys are tokens gid and gid + 8, its values tokens 2 tig, 2 tig + 1 and those + 8.
+        int here = 0, tile = t0;
+        {
+            for (; tile < coded_end; tile++) {
+                send(tile + kSteps - 1);
+                wait_groups<kSteps - 1>();
+                __syncwarp();
+                if (coded >> here & 1) {
+                    const uint32_t from = steps + here * Layout::kBytes;
+                    uint32_t kr[2][kK / 4], vr[4][kV / 4];
+                    float ks, vs;
+                    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(ks), "=f"(vs) : "r"(from + 2 * Layout::kCodes));
+#pragma unroll
+                    for (int i = 0; i < kK; i += kKLoad) {
+                        load_shared<kKLoad>(kr[0] + i / 4, from + Layout::key(gid, tig * kK + i));
+                        load_shared<kKLoad>(kr[1] + i / 4, from + Layout::key(gid + 8, tig * kK + i));
+                    }
+#pragma unroll
+                    for (int i = 0; i < kV; i += kVLoad)
+#pragma unroll
+                        for (int j = 0; j < 4; j++)
+                            load_shared<kVLoad>(vr[j] + i / 4, from + Layout::kCodes + Layout::value(2 * tig + j / 2 * 8 + j % 2, gid * kV + i));
+                    float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                    for (int s = 0; s < D / 16; s++) {
+                        const uint32_t lo = kr[0][s] ^ 0x80808080u, hi = kr[1][s] ^ 0x80808080u;
+                        const uint32_t f[4] = {sub2(__byte_perm(lo, 0x64646464u, 0x4140)), sub2(__byte_perm(hi, 0x64646464u, 0x4140)),
+                                               sub2(__byte_perm(lo, 0x64646464u, 0x4342)), sub2(__byte_perm(hi, 0x64646464u, 0x4342))};
+                        mma16816(c, f, q[s][0], q[s][1]);
+                    }
+                    const float f0 = qs[0] * ks, f1 = qs[1] * ks;
+                    float s[4] = {c[0] * f0, c[1] * f1, c[2] * f0, c[3] * f1};
+                    r.weights(s);
+                    const Weights16 p(s);
+#pragma unroll
+                    for (int i = 0; i < D / 32; i++) {
+                        // four channels of four tokens to the fragments of two MMAs
+                        const uint32_t x0 = vr[0][i] ^ 0x80808080u, x1 = vr[1][i] ^ 0x80808080u;
+                        const uint32_t x2 = vr[2][i] ^ 0x80808080u, x3 = vr[3][i] ^ 0x80808080u;
+#pragma unroll
+                        for (int u = 0; u < 2; u++) {
+                            const uint32_t lo = __byte_perm(x0, x1, u ? 0x7362 : 0x5140), hi = __byte_perm(x2, x3, u ? 0x7362 : 0x5140);
+                            const uint32_t f[4] = {sub2(__byte_perm(lo, 0x64646464u, 0x4140)), sub2(__byte_perm(lo, 0x64646464u, 0x4342)),
+                                                   sub2(__byte_perm(hi, 0x64646464u, 0x4140)), sub2(__byte_perm(hi, 0x64646464u, 0x4342))};
+                            float w[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                            mma16816(w, f, p.p0, p.p1);
+                            float *o = r.o[2 * i + u];
+                            o[0] += w[0] * vs, o[1] += w[1] * vs, o[2] += w[2] * vs, o[3] += w[3] * vs;
+                        }
+                    }
+                }
+                __syncwarp();  // the step's place is sent to again
+                here = here + 1 == kSteps ? 0 : here + 1;
+            }
+        }
+
+        for (; tile < t1; tile++) {
             const int tok = tile * kTile + warp * 16;
-            send(tile + kSteps - 1);
-            wait_groups<kSteps - 1>();
-            __syncwarp();
-            if (coded >> here & 1) {
-                const uint32_t from = steps + here * Layout::kBytes;
-                uint32_t kr[2][kK / 4], vr[4][kV / 4];
-                float ks, vs;
-                asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(ks), "=f"(vs) : "r"(from + 2 * Layout::kCodes));
-#pragma unroll
-                for (int i = 0; i < kK; i += kKLoad) {
-                    load_shared<kKLoad>(kr[0] + i / 4, from + Layout::key(gid, tig * kK + i));
-                    load_shared<kKLoad>(kr[1] + i / 4, from + Layout::key(gid + 8, tig * kK + i));
-                }
-#pragma unroll
-                for (int i = 0; i < kV; i += kVLoad)
-#pragma unroll
-                    for (int j = 0; j < 4; j++)
-                        load_shared<kVLoad>(vr[j] + i / 4, from + Layout::kCodes + Layout::value(2 * tig + j / 2 * 8 + j % 2, gid * kV + i));
-                float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                for (int s = 0; s < D / 16; s++) {
-                    const uint32_t lo = kr[0][s] ^ 0x80808080u, hi = kr[1][s] ^ 0x80808080u;
-                    const uint32_t f[4] = {sub2(__byte_perm(lo, 0x64646464u, 0x4140)), sub2(__byte_perm(hi, 0x64646464u, 0x4140)),
-                                           sub2(__byte_perm(lo, 0x64646464u, 0x4342)), sub2(__byte_perm(hi, 0x64646464u, 0x4342))};
-                    mma16816(c, f, q[s][0], q[s][1]);
-                }
-                const float f0 = qs[0] * ks, f1 = qs[1] * ks;
-                const float s[4] = {c[0] * f0, c[1] * f1, c[2] * f0, c[3] * f1};
-                uint32_t p0, p1;
-                r.weights(s, p0, p1);
-#pragma unroll
-                for (int i = 0; i < D / 32; i++) {
-                    // four channels of four tokens to the fragments of two MMAs
-                    const uint32_t x0 = vr[0][i] ^ 0x80808080u, x1 = vr[1][i] ^ 0x80808080u;
-                    const uint32_t x2 = vr[2][i] ^ 0x80808080u, x3 = vr[3][i] ^ 0x80808080u;
-#pragma unroll
-                    for (int u = 0; u < 2; u++) {
-                        const uint32_t lo = __byte_perm(x0, x1, u ? 0x7362 : 0x5140), hi = __byte_perm(x2, x3, u ? 0x7362 : 0x5140);
-                        const uint32_t f[4] = {sub2(__byte_perm(lo, 0x64646464u, 0x4140)), sub2(__byte_perm(lo, 0x64646464u, 0x4342)),
-                                               sub2(__byte_perm(hi, 0x64646464u, 0x4140)), sub2(__byte_perm(hi, 0x64646464u, 0x4342))};
-                        float w[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                        mma16816(w, f, p0, p1);
-                        float *o = r.o[2 * i + u];
-                        o[0] += w[0] * vs, o[1] += w[1] * vs, o[2] += w[2] * vs, o[3] += w[3] * vs;
-                    }
-                }
+            if (tok >= len) break;
+            const int slot = a.slot_of ? a.slot_of[seq] : seq;
+            if (slot < 0 || slot >= a.c.slots) {
+                set_status(a.status, ENTRO_E_INVAL);
             } else {
-                const int slot = a.slot_of ? a.slot_of[seq] : seq;
-                const bool slot_ok = slot >= 0 && slot < a.c.slots;
-                if (tok >= full && tok < len && !slot_ok) set_status(a.status, ENTRO_E_INVAL);
-                if (tok >= full && tok < len && slot_ok) {
-                    // up to 16 tokens of the open block, in 16 bits
-                    const int64_t base = (static_cast<int64_t>(slot) * a.c.kv + h) * P + (tok & (P - 1));
-                    const T *kt = static_cast<const T *>(a.c.tail[0]) + base * D, *vt = static_cast<const T *>(a.c.tail[1]) + base * D;
-                    const int n = len - tok;  // tokens of the step that exist, if below 16
-                    float c[4] = {0.0f, 0.0f, 0.0f, 0.0f}, inverse;
-                    {
-                        uint32_t x[2][D / 8], top = 0;
+                // Up to 16 tokens of the open block, in 16 bits: their products take them as they are, so that neither
+                // a large number nor an infinity changes what the others count.
+                const int64_t base = (static_cast<int64_t>(slot) * a.c.kv + h) * P + (tok & (P - 1));
+                const T *kt = static_cast<const T *>(a.c.tail[0]) + base * D, *vt = static_cast<const T *>(a.c.tail[1]) + base * D;
+                const int n = len - tok;  // tokens of the step that exist, if below 16
+                float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                {
+                    uint32_t x[2][D / 8], raw[D / 8];
 #pragma unroll
-                        for (int j = 0; j < 2; j++) {
-                            if (gid + 8 * j < n) {
-                                load_bytes<D / 2>(x[j], kt + (gid + 8 * j) * D + tig * kK);
-                            } else {
-#pragma unroll
-                                for (int i = 0; i < D / 8; i++) x[j][i] = 0;
-                            }
-#pragma unroll
-                            for (int i = 0; i < D / 8; i++) top = __vmaxu2(top, x[j][i] & 0x7FFF7FFFu);
-                        }
-                        top = __reduce_max_sync(~0u, max(top & 0xFFFF, top >> 16));
-                        const float f = fit_factor<T>(top, inverse);
-#pragma unroll
-                        for (int s = 0; s < D / 16; s++) {
-                            const uint32_t fr[4] = {to_f16x2<T>(x[0][2 * s], f), to_f16x2<T>(x[1][2 * s], f),
-                                                    to_f16x2<T>(x[0][2 * s + 1], f), to_f16x2<T>(x[1][2 * s + 1], f)};
-                            mma16816(c, fr, q[s][0], q[s][1]);
-                        }
-                    }
-                    const float f0 = qs[0] * inverse, f1 = qs[1] * inverse;
-                    const float s[4] = {gid < n ? c[0] * f0 : -INFINITY, gid < n ? c[1] * f1 : -INFINITY,
-                                        gid + 8 < n ? c[2] * f0 : -INFINITY, gid + 8 < n ? c[3] * f1 : -INFINITY};
-                    uint32_t p0, p1;
-                    r.weights(s, p0, p1);
-                    uint32_t y[4][D / 16], top = 0;
-#pragma unroll
-                    for (int j = 0; j < 4; j++) {
-                        const int t = 2 * tig + j / 2 * 8 + j % 2;
-                        if (t < n) {
-                            load_bytes<D / 4>(y[j], vt + t * D + gid * kV);
+                    for (int j = 0; j < 2; j++) {
+                        if (gid + 8 * j < n) {
+                            load_bytes<D / 2>(x[j], kt + (gid + 8 * j) * D + tig * kK);
                         } else {
 #pragma unroll
-                            for (int i = 0; i < D / 16; i++) y[j][i] = 0;
+                            for (int i = 0; i < D / 8; i++) x[j][i] = 0;
                         }
-#pragma unroll
-                        for (int i = 0; i < D / 16; i++) top = __vmaxu2(top, y[j][i] & 0x7FFF7FFFu);
                     }
-                    top = __reduce_max_sync(~0u, max(top & 0xFFFF, top >> 16));
-                    const float f = fit_factor<T>(top, inverse);
+                    if (kBf16) load_bytes<D / 2>(raw, q_row(gid) + tig * kK);
 #pragma unroll
-                    for (int i = 0; i < D / 16; i++) {
-                        uint32_t z[4];
+                    for (int s = 0; s < D / 16; s++) {
+                        const uint32_t f[4] = {x[0][2 * s], x[1][2 * s], x[0][2 * s + 1], x[1][2 * s + 1]};
+                        if (kBf16) mma16816_bf16(c, f, gid < heads ? raw[2 * s] : 0u, gid < heads ? raw[2 * s + 1] : 0u);
+                        else mma16816(c, f, q[s][0], q[s][1]);
+                    }
+                }
+                float s[4];
 #pragma unroll
-                        for (int j = 0; j < 4; j++) z[j] = to_f16x2<T>(y[j][i], f);
-                        const uint32_t fr[4] = {__byte_perm(z[0], z[1], 0x5410), __byte_perm(z[0], z[1], 0x7632),
-                                                __byte_perm(z[2], z[3], 0x5410), __byte_perm(z[2], z[3], 0x7632)};
+                for (int i = 0; i < 4; i++) s[i] = gid + i / 2 * 8 < n ? c[i] * a.scale_log2 : -INFINITY;
+                r.weights(s);
+                // The weights: fp16, or a pair of bfloat16 whose sum is as near (2^-18).
+                const Weights16 p(s);
+                uint32_t hi[2], lo[2];
+#pragma unroll
+                for (int i = 0; i < 2; i++) {
+                    const uint32_t x = Half<__nv_bfloat16>::pack(s[2 * i], s[2 * i + 1]);
+                    const float2 f = Half<__nv_bfloat16>::widen(x);
+                    hi[i] = transpose8x8(x);
+                    lo[i] = transpose8x8(Half<__nv_bfloat16>::pack(s[2 * i] - f.x, s[2 * i + 1] - f.y));
+                }
+                uint32_t y[4][D / 16];
+#pragma unroll
+                for (int j = 0; j < 4; j++) {
+                    const int t = 2 * tig + j / 2 * 8 + j % 2;
+                    if (t < n) {
+                        load_bytes<D / 4>(y[j], vt + t * D + gid * kV);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < D / 16; i++) y[j][i] = 0;
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < D / 16; i++) {
+                    uint32_t f[4] = {__byte_perm(y[0][i], y[1][i], 0x5410), __byte_perm(y[0][i], y[1][i], 0x7632),
+                                     __byte_perm(y[2][i], y[3][i], 0x5410), __byte_perm(y[2][i], y[3][i], 0x7632)};
+                    if (kBf16) {
+                        mma16816_bf16(r.o[i], f, hi[0], hi[1]);
+                        // (infinities count once: the remainders may be 0 or below)
+#pragma unroll
+                        for (int j = 0; j < 4; j++) f[j] &= ~__vcmpeq2(f[j] & Half<T>::kExp, Half<T>::kExp);
+                        mma16816_bf16(r.o[i], f, lo[0], lo[1]);
+                    } else {
                         float w[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                        mma16816(w, fr, p0, p1);
+                        mma16816(w, f, p.p0, p.p1);
 #pragma unroll
-                        for (int j = 0; j < 4; j++) r.o[i][j] += w[j] * inverse;
+                        for (int j = 0; j < 4; j++) r.o[i][j] += w[j];
                     }
                 }
             }
-            __syncwarp();  // the step's place is sent to again
-            here = here + 1 == kSteps ? 0 : here + 1;
         }
         wait_groups<0>();
 
