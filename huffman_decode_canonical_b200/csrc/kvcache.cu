@@ -10,6 +10,7 @@
 // holds does not depend on how its tokens arrived.
 #include <algorithm>
 #include <cstring>
+#include <type_traits>
 
 #include "launch.h"
 #include "sm100.cuh"
@@ -419,15 +420,18 @@ __device__ __forceinline__ void load_bytes(uint32_t *r, const void *p) {
     }
 }
 // A power of two that brings numbers of at most this magnitude (the bits of a
-// 16-bit float without its sign) near 2^14, and its inverse: they then fit fp16,
-// and those that lose bits there are below 2^-27 of the largest.
+// 16-bit float without its sign) near 2^14, and its inverse.  A bfloat16 then fits
+// fp16 exactly if its exponent is at most 31 below the largest: `exact_from` has the
+// bits of the smallest that does.
 template <typename T>
-__device__ __forceinline__ float fit_factor(uint32_t top, float &inverse) {
+__device__ __forceinline__ float fit_factor(uint32_t top, float &inverse, int &exact_from) {
+    exact_from = 0;
     if (Half<T>::kExp == 0x7C007C00u) {  // fp16 already
         inverse = 1.0f;
         return 1.0f;
     }
     const int e = min(max(static_cast<int>(top >> 7), 28), 254);  // biased exponent
+    exact_from = (e - 31) * 128;
     inverse = __uint_as_float(static_cast<uint32_t>(e - 14) << 23);
     return __uint_as_float(static_cast<uint32_t>(254 + 14 - e) << 23);
 }
@@ -436,6 +440,30 @@ __device__ __forceinline__ uint32_t to_f16x2(uint32_t v, float factor) {
     if (Half<T>::kExp == 0x7C007C00u) return v;
     const float2 f = Half<T>::widen(v);
     return Half<__half>::pack(f.x * factor, f.y * factor);
+}
+
+// Scores of a step of coded tokens by products in 32 bits, of code times scale as they stand: for queries whose channels
+// lie too far apart for one factor.  As in the MMA, this thread's are tokens gid and gid + 8 of heads 2 tig and 2 tig + 1
+// (q0, q1); `from` holds the step's keys, in StepLayout.
+template <typename T, int D>
+__device__ __forceinline__ void wide_scores(float *s, uint32_t from, float scale, const T *q0, const T *q1) {
+    const int gid = threadIdx.x % 32 / 4;
+    s[0] = s[1] = s[2] = s[3] = 0.0f;
+#pragma unroll 1
+    for (int d = 0; d < D; d += 4) {
+        uint32_t k[2];
+        load_shared<4>(k, from + StepLayout<D>::key(gid, d));
+        load_shared<4>(k + 1, from + StepLayout<D>::key(gid + 8, d));
+        const uint2 x = __ldg(reinterpret_cast<const uint2 *>(q0 + d)), y = __ldg(reinterpret_cast<const uint2 *>(q1 + d));
+        const float2 xs[2] = {Half<T>::widen(x.x), Half<T>::widen(x.y)}, ys[2] = {Half<T>::widen(y.x), Half<T>::widen(y.y)};
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const float a = i % 2 ? xs[i / 2].y : xs[i / 2].x, b = i % 2 ? ys[i / 2].y : ys[i / 2].x;
+            const float lo = static_cast<float>(static_cast<int8_t>(k[0] >> (8 * i))) * scale;
+            const float hi = static_cast<float>(static_cast<int8_t>(k[1] >> (8 * i))) * scale;
+            s[0] = fmaf(a, lo, s[0]), s[1] = fmaf(b, lo, s[1]), s[2] = fmaf(a, hi, s[2]), s[3] = fmaf(b, hi, s[3]);
+        }
+    }
 }
 
 // A warp's running softmax over the tokens it has seen, for 8 query heads: this
@@ -583,6 +611,7 @@ __global__ void __launch_bounds__(kAttendThreads, 4) attend_kernel(const AttendA
         // Q as the second operand: head gid, channels tig D / 4 + 4 s + 0 .. 3 in step s
         uint32_t q[D / 16][2];
         float mine = 0.0f;
+        bool wide = false;  // some query's channels lie too far apart for fp16 (the warp's)
         auto q_row = [&](int head) { return static_cast<const T *>(a.q) + seq * a.q_token + (head0 + min(head, heads - 1)) * a.q_head; };
         {
             uint32_t raw[D / 8], top = 0;
@@ -592,7 +621,14 @@ __global__ void __launch_bounds__(kAttendThreads, 4) attend_kernel(const AttendA
             top = max(top & 0xFFFF, top >> 16);
             top = max(top, __shfl_xor_sync(~0u, top, 1));
             top = max(top, __shfl_xor_sync(~0u, top, 2));
-            const float f = fit_factor<T>(top, mine);
+            int exact_from;
+            const float f = fit_factor<T>(top, mine, exact_from);
+            if (kBf16) {
+                uint32_t low = ~0u;  // the smallest magnitude but 0, less one
+#pragma unroll
+                for (int i = 0; i < D / 8; i++) low = __vminu2(low, __vsub2(raw[i] & 0x7FFF7FFFu, 0x00010001u));
+                wide = __any_sync(~0u, static_cast<int>(min(low & 0xFFFF, low >> 16)) + 1 < exact_from);
+            }
 #pragma unroll
             for (int i = 0; i < D / 8; i++) q[i / 2][i % 2] = gid < heads ? to_f16x2<T>(raw[i], f) : 0u;
             mine *= a.scale_log2;
@@ -603,7 +639,7 @@ __global__ void __launch_bounds__(kAttendThreads, 4) attend_kernel(const AttendA
         r.clear();
         // Steps of coded tokens: a thread's keys are tokens gid and gid + 8, its values tokens 2 tig, 2 tig + 1 and those + 8.
         int here = 0, tile = t0;
-        {
+        auto coded_steps = [&](auto by_products) {
             for (; tile < coded_end; tile++) {
                 send(tile + kSteps - 1);
                 wait_groups<kSteps - 1>();
@@ -633,6 +669,11 @@ __global__ void __launch_bounds__(kAttendThreads, 4) attend_kernel(const AttendA
                     }
                     const float f0 = qs[0] * ks, f1 = qs[1] * ks;
                     float s[4] = {c[0] * f0, c[1] * f1, c[2] * f0, c[3] * f1};
+                    if (decltype(by_products)::value) {
+                        wide_scores<T, D>(s, from, ks, q_row(2 * tig), q_row(2 * tig + 1));
+#pragma unroll
+                        for (int i = 0; i < 4; i++) s[i] *= a.scale_log2;
+                    }
                     r.weights(s);
                     const Weights16 p(s);
 #pragma unroll
@@ -655,7 +696,9 @@ __global__ void __launch_bounds__(kAttendThreads, 4) attend_kernel(const AttendA
                 __syncwarp();  // the step's place is sent to again
                 here = here + 1 == kSteps ? 0 : here + 1;
             }
-        }
+        };
+        if (kBf16 && wide) coded_steps(std::true_type());
+        else coded_steps(std::false_type());
 
         for (; tile < t1; tile++) {
             const int tok = tile * kTile + warp * 16;

@@ -41,6 +41,28 @@ def test_a_large_number_of_the_open_block(dim):
         _check_attention(c, 4, q=q.to(BF16))
 
 
+@pytest.mark.parametrize("dim,page,kv,group", [(64, 16, 2, 4), (96, 32, 1, 3), (128, 64, 2, 8), (128, 16, 1, 12)])
+def test_channels_of_the_query(dim, page, kv, group):
+    """Queries with a channel 2^60 times the others where the keys hold 0, or channels that span 2^200: coded and open blocks."""
+    c = Case(3, kv, dim, page, BF16, width=-(-300 // page), seed=22)
+    n = [300, 2 * page, page + 5]
+    k, v = c.tokens(sum(n)), c.tokens(sum(n))
+    k[..., 5] = 0
+    c.append(n, packed=(k, v))
+    q = torch.randn(3, kv * group, dim, generator=c.g)
+    q[:, ::2, 5] = 2.0 ** 60
+    q[1, 1] *= _spread(dim, -120, 0, c.g)
+    q[2, 0, 5] = 2.0 ** 31  # the last that one factor fits, and the first that it does not
+    q[2, 1, 5] = 2.0 ** 33
+    _check_attention(c, kv * group, q=q.to(BF16))
+    q = torch.randn(3, kv * group, dim, generator=c.g)
+    q[0] = 0
+    q[1, :, :] = 0
+    q[1, 0, 9], q[1, 0, 10] = 2.0 ** -133, 2.0 ** -100  # the smallest number, beside another and alone
+    q[1, 1, 9] = 2.0 ** -133
+    _check_attention(c, kv * group, q=q.to(BF16))
+
+
 def _expect(q, k, v, keep):
     """(o, sum p |v|, largest sum of the scores' magnitudes) over the tokens that are kept, 64 bits: q [heads, dim]"""
     g = q.shape[0] // k.shape[1]
