@@ -513,6 +513,10 @@ struct Running {
     }
 };
 
+// What sums of weights make of an output: 1 / l; nothing where there were no tokens; NaN where there were, but all scored
+// -infinity (their sum is marked by a negative number, which counts nothing beside other sums).
+__device__ __forceinline__ float by_sum(float l) { return l == 0.0f ? 0.0f : l < 0.0f ? __int_as_float(0x7FC00000) : 1.0f / l; }
+
 // Weights as the P^T operand in fp16 (2^-11 of a weight at most).
 struct Weights16 {
     uint32_t p0, p1;
@@ -577,7 +581,8 @@ __global__ void __launch_bounds__(kAttendThreads, 4) attend_kernel(const AttendA
         const int32_t *pages = a.table + seq * a.table_stride;
 
         // Steps of 16 tokens, kSteps - 1 of them on their way; this warp's tiles up to `coded_end` are of coded blocks.  A
-        // step on a page that does not exist copies nothing; bit x of `coded` says of the step in place x whether it did.
+        // step on a page that does not exist copies nothing; bit x of `coded` says of the step in place x whether it did,
+        // and its bit 31 whether this warp has had any token.
         const int coded_end = min(t1, (full - warp * 16 + kTile - 1) / kTile);
         uint32_t coded = 0;
         int place = 0;  // of the next step to be sent
@@ -598,7 +603,7 @@ __global__ void __launch_bounds__(kAttendThreads, 4) attend_kernel(const AttendA
                         copy_async16(to + Layout::kCodes + Layout::value(row, byte), a.c.codes[1] + from + piece * 16);
                     }
                     if (lane < 2) copy_async4(to + 2 * Layout::kCodes + lane * 4, a.c.scale[lane] + block);
-                    coded |= 1u << place;
+                    coded |= 1u << place | 1u << 31;
                 } else {
                     set_status(a.status, ENTRO_E_INVAL);
                 }
@@ -707,6 +712,7 @@ __global__ void __launch_bounds__(kAttendThreads, 4) attend_kernel(const AttendA
             if (slot < 0 || slot >= a.c.slots) {
                 set_status(a.status, ENTRO_E_INVAL);
             } else {
+                coded |= 1u << 31;
                 // Up to 16 tokens of the open block, in 16 bits: their products take them as they are, so that neither
                 // a large number nor an infinity changes what the others count.
                 const int64_t base = (static_cast<int64_t>(slot) * a.c.kv + h) * P + (tok & (P - 1));
@@ -780,6 +786,11 @@ __global__ void __launch_bounds__(kAttendThreads, 4) attend_kernel(const AttendA
 
         // the four warps' parts meet in shared memory
         __syncthreads();
+        if (coded >> 31) {
+#pragma unroll
+            for (int x = 0; x < 2; x++)
+                if (r.m[x] == -INFINITY && r.l[x] == 0.0f) r.l[x] = -1.0f;
+        }
 #pragma unroll
         for (int x = 4; x < 32; x *= 2) {
             r.l[0] += __shfl_xor_sync(~0u, r.l[0], x);
@@ -814,7 +825,7 @@ __global__ void __launch_bounds__(kAttendThreads, 4) attend_kernel(const AttendA
                 o1 += f * sm_o[w][head][d + 1];
             }
             if (whole) {
-                const float by = l == 0.0f ? 0.0f : 1.0f / l;
+                const float by = by_sum(l);
                 T *out = static_cast<T *>(a.out) + seq * a.out_token + (head0 + head) * a.out_head + d;
                 *reinterpret_cast<uint32_t *>(out) = Half<T>::pack(o0 * by, o1 * by);
             } else {
@@ -890,7 +901,7 @@ __global__ void __launch_bounds__(kAttendThreads) join_kernel(const AttendArgs a
     if (half == 1) half_o[tid - 64] = o;
     __syncthreads();
     if (half == 0 && d < D) {
-        const float by = sum == 0.0f ? 0.0f : 1.0f / sum;
+        const float by = by_sum(sum);
         T *out = static_cast<T *>(a.out) + seq * a.out_token + head * a.out_head + d;
         *reinterpret_cast<uint32_t *>(out) = Half<T>::pack((o.x + half_o[tid].x) * by, (o.y + half_o[tid].y) * by);
     }

@@ -132,7 +132,7 @@ __device__ __forceinline__ void row_by_row(const PromptArgs &a, int head, int64_
     for (int x = 16; x; x /= 2) l += __shfl_xor_sync(~0u, l, x);
     T *out = static_cast<T *>(a.out) + q_row * a.out_token + head * a.out_head;
 #pragma unroll
-    for (int i = 0; i < D / 32; i++) out[i * 32 + lane] = static_cast<T>(l == 0.0f ? 0.0f : o[i] / l);
+    for (int i = 0; i < D / 32; i++) out[i * 32 + lane] = static_cast<T>(visible > 0 ? o[i] / l : 0.0f);
 }
 
 // What a CTA works on: 256 queries of a head.
@@ -298,7 +298,7 @@ __device__ __forceinline__ void join_parts(const PromptArgs &a, const PromptItem
                     o[0] = fmaf(f, x.x, o[0]), o[1] = fmaf(f, x.y, o[1]), o[2] = fmaf(f, x.z, o[2]), o[3] = fmaf(f, x.w, o[3]);
                     o[4] = fmaf(f, y.x, o[4]), o[5] = fmaf(f, y.y, o[5]), o[6] = fmaf(f, y.z, o[6]), o[7] = fmaf(f, y.w, o[7]);
                 }
-            const float by = sum == 0.0f ? 0.0f : 1.0f / sum;
+            const float by = sum == 0.0f ? 0.0f : sum < 0.0f ? __int_as_float(0x7FC00000) : 1.0f / sum;
             uint32_t h[4];
 #pragma unroll
             for (int z = 0; z < 4; z++) h[z] = sum == 0.0f ? 0u : Half<T>::pack(o[2 * z] * by, o[2 * z + 1] * by);
@@ -637,13 +637,20 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                 tc_fence_after();
             }
             if (!ok) break;
+            // (the last key of this row once more: over the loop above there is no register for it)
+            int last = tid;
+            asm volatile("" : "+r"(last));
+            last += it.row0 + it.offset;
+            // Keys that all score -infinity leave no softmax: NaN (0 / 0), unlike no keys at all.
             if (a.parts > 1) {
+                // a part's row of such keys says so by a negative sum, which counts nothing beside those of other parts
+                if (l == 0.0f && nt > 0 && last >= 0) l = -1.0f;
                 join_parts<T, D>(a, it, base, ot, m, l, nt > 0, smem_u32(special));
                 joined = true;
                 break;
             }
             if (first < it.qlen) {
-                const float by = l == 0.0f ? 0.0f : 1.0f / l;
+                const float by = 1.0f / l;
                 T *out = static_cast<T *>(a.out) + (static_cast<int64_t>(it.q0) + row) * a.out_token + it.head * a.out_head;
 #pragma unroll 1
                 for (int x = 0; x < D; x += 32) {
@@ -658,7 +665,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                             uint32_t h[4];
 #pragma unroll
                             for (int z = 0; z < 4; z++)
-                                h[z] = l == 0.0f ? 0u : Half<T>::pack(__uint_as_float(o[y + 2 * z]) * by, __uint_as_float(o[y + 2 * z + 1]) * by);
+                                h[z] = last < 0 ? 0u : Half<T>::pack(__uint_as_float(o[y + 2 * z]) * by, __uint_as_float(o[y + 2 * z + 1]) * by);
                             *reinterpret_cast<uint4 *>(out + x + y) = make_uint4(h[0], h[1], h[2], h[3]);
                         }
                     }

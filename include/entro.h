@@ -285,8 +285,9 @@ ENTRO_API int entro_matmul_i8(const int8_t *d_q, int64_t ldq, const float *d_x_s
  * sees keys j <= i + klen - qlen, so a prompt's next part attends to what came
  * before it.  Head h reads key head h / (heads / kv_heads).
  *   out[i,h] = sum_j p_j v_j,  p = softmax_j(scale q[i,h] . k_j),  scale > 0
- * A query that sees no key gets 0; rows of no sequence are left as they are; what
- * the mask hides does not count, infinities and NaN included.  Scores, sums and
+ * A query that sees no key gets 0 (one whose keys all score -infinity NaN); rows of
+ * no sequence are left as they are; what the mask hides does not count, infinities
+ * and NaN included.  Scores, sums and
  * outputs are taken in fp32, the weights p rounded to `type`; results do not
  * depend on the other sequences of the batch, unless the whole call's few queries
  * leave SMs free to share keys (1024 keys a sequence on average or more): then the
@@ -348,7 +349,8 @@ ENTRO_API int entro_kv_read(const entro_kv_cache *cache, void *d_k, int64_t k_to
 /* Attention of one token of each sequence over its cache: for b < batch and
  * h < heads (a multiple of kv_heads; head h reads key head h / (heads / kv_heads)),
  *   out[b,h] = sum_j p_j v_j,  p = softmax_j(scale q[b,h] . k_j),  j < d_lens[b]
- * over the values that the cache stands for.  A sequence without tokens gets 0.
+ * over the values that the cache stands for.  A sequence without tokens gets 0 (one
+ * whose tokens all score -infinity NaN).
  * Scores, sums and outputs are taken in fp32, the weights p rounded to fp16; a
  * result does not depend on when it is computed (no atomics), but on the batch,
  * which decides how the work is split.  scale > 0.  d_work: device memory of at
