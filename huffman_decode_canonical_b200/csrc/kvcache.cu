@@ -186,16 +186,10 @@ __device__ __forceinline__ bool packed_range(const ReadArgs &a, int b, int &begi
     return begin >= 0 && begin <= end && end <= a.tokens;
 }
 
-// Cached tokens back to 16 bits: code times scale in 32 bits, rounded once.  A
-// warp takes a token at a time; bound by memory: 36000 tokens of 8 x 128 in 46 us, 4.8 TB/s.
+// One cached token back to 16 bits, by a warp: code times scale in 32 bits, rounded once.
 template <typename T, int D>
-__global__ void __launch_bounds__(256) read_kernel(const ReadArgs a) {
+__device__ __forceinline__ void read_token(const ReadArgs &a, int64_t t) {
     const int lane = threadIdx.x % 32, P = 1 << a.c.log_page;
-    const int64_t t = blockIdx.x * 8LL + threadIdx.x / 32;
-    int begin, end;
-    for (int64_t b = blockIdx.x * 256LL + threadIdx.x; b < a.batch; b += gridDim.x * 256LL)
-        if (!packed_range(a, static_cast<int>(b), begin, end)) set_status(a.status, ENTRO_E_INVAL);
-    if (t >= a.tokens) return;
     // the last sequence that begins at or before t
     int lo = 0, hi = a.batch;
     while (hi - lo > 1) {
@@ -204,6 +198,7 @@ __global__ void __launch_bounds__(256) read_kernel(const ReadArgs a) {
         else hi = mid;
     }
     const int b = lo;
+    int begin, end;
     if (!packed_range(a, b, begin, end) || t < begin || t >= end) return;  // a token of no sequence: left as it is
     const int pos = static_cast<int>(t) - begin, block = pos >> a.c.log_page;
     const int slot = a.slot_of ? a.slot_of[b] : b;
@@ -244,6 +239,17 @@ __global__ void __launch_bounds__(256) read_kernel(const ReadArgs a) {
         out[0] = make_uint4(o[0], o[1], o[2], o[3]);
         out[1] = make_uint4(o[4], o[5], o[6], o[7]);
     }
+}
+
+// Bound by memory: 36000 tokens of 8 x 128 in 46 us, 4.8 TB/s.
+template <typename T, int D>
+__global__ void __launch_bounds__(256) read_kernel(const ReadArgs a) {
+    const int64_t t = blockIdx.x * 8LL + threadIdx.x / 32;
+    if (t < a.tokens) read_token<T, D>(a, t);
+    // offsets are reported whether a token finds them or not (last: the tokens do not wait for it)
+    int begin, end;
+    for (int64_t b = blockIdx.x * 256LL + threadIdx.x; b < a.batch; b += gridDim.x * 256LL)
+        if (!packed_range(a, static_cast<int>(b), begin, end)) set_status(a.status, ENTRO_E_INVAL);
 }
 
 // ------------------------------------------------------------------ attention of single tokens
