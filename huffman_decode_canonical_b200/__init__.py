@@ -22,6 +22,7 @@ from typing import List, NamedTuple, Optional, Sequence, Union
 
 import numpy as np
 import torch
+from torch.autograd.forward_ad import unpack_dual
 
 from . import _binding as _fast  # built with the library (build.py)
 
@@ -400,8 +401,8 @@ class _on:
 
 
 def _check_inputs(index: int, tensors, names):
-    """Refuses what the kernels must not be given: tensors of other devices, or ones that ask for gradients; a status
-    that is no int32 word (the last one named so)."""
+    """Refuses what the kernels must not be given: tensors of other devices, or ones that ask for gradients (backward or
+    forward: a tangent would be lost); a status that is no int32 word (the last one named so)."""
     if index < 0:
         raise ValueError("expected CUDA tensors")
     if names[-1] == "status" and tensors[-1] is not None and (tensors[-1].dtype is not torch.int32 or tensors[-1].numel() < 1):
@@ -413,6 +414,8 @@ def _check_inputs(index: int, tensors, names):
             if t.get_device() != index:
                 raise ValueError(f"{name} is on {t.device}, not on cuda:{index}")
             raise ValueError(f"{name} requires a gradient: this call has none (use torch.no_grad())")
+        if t is not None and t.is_floating_point() and unpack_dual(t).tangent is not None:
+            raise ValueError(f"{names[[u is t for u in tensors].index(True)]} is a dual tensor: this call has no forward-mode gradient")
 
 
 def _pitch(cols: int) -> int:

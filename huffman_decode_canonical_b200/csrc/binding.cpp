@@ -32,14 +32,15 @@ decltype(&entro_kv_attend) f_attend;
 using at::ScalarType;
 using at::Tensor;
 
-// A tensor argument on device `index` (-1: sets it), without a gradient to take; null if it is none of that.
+// A tensor argument on device `index` (-1: sets it), without a gradient to take or a tangent to carry on; null if it is
+// none of that.
 const Tensor *tensor(PyObject *o, int &index) {
     if (!THPVariable_CheckExact(o)) return nullptr;
     const Tensor &t = THPVariable_Unpack(o);
     if (!t.is_cuda() || t.layout() != at::kStrided) return nullptr;
     const int at = t.get_device();
     if (index < 0) index = at;
-    if (at != index || (t.requires_grad() && c10::GradMode::is_enabled())) return nullptr;
+    if (at != index || (t.requires_grad() && c10::GradMode::is_enabled()) || t._fw_grad(0).defined()) return nullptr;
     return &t;
 }
 // The same, or None (which leaves `t` null).
