@@ -24,10 +24,9 @@ import numpy as np
 import torch
 from torch.autograd.forward_ad import unpack_dual
 
-from . import _binding as _fast  # built with the library (build.py)
-
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libentro.so")
+BINDING_PATH = os.path.join(_HERE, "_binding.so")
 
 OK = 0
 E_INVAL, E_LIMIT, E_FORMAT, E_CORRUPT, E_OVERRUN, E_NOMEM, E_CUDA, E_TIMEOUT = -1, -2, -3, -4, -5, -6, -7, -8
@@ -76,10 +75,14 @@ EXPORTS = ["entro_encode", "entro_blob_from_bytes", "entro_blob_bytes", "entro_b
            "entro_kv_append", "entro_kv_read", "entro_kv_attend_workspace", "entro_kv_attend", "entro_attention_prompt"]
 
 
-def _load() -> ctypes.CDLL:
-    if not os.path.exists(LIB_PATH):
-        raise ImportError(f"{LIB_PATH} is missing: build it with `python huffman_decode_canonical_b200/build.py` "
+def _built(path: str):
+    if not os.path.exists(path):
+        raise ImportError(f"{path} is missing: build it with `python huffman_decode_canonical_b200/build.py` "
                           "(there is no CPU fallback)")
+
+
+def _load() -> ctypes.CDLL:
+    _built(LIB_PATH)
     lib = ctypes.CDLL(LIB_PATH)
     P, I32, I64, U64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_uint64
     F32 = ctypes.c_float
@@ -123,11 +126,27 @@ def _load() -> ctypes.CDLL:
     return lib
 
 
+class _NoFast:
+    """In place of the binding's module where torch knows no CUDA: the host side needs none."""
+
+    def __getattr__(self, name):
+        return lambda *a: None
+
+
+def _load_binding():
+    """The usual calls of the operators around the coded weights, checked and made without the interpreter's part: each
+    returns None for anything that is not the plain valid case, and the function here goes on."""
+    if torch.version.cuda is None:
+        return _NoFast()
+    _built(BINDING_PATH)
+    from . import _binding
+    _binding.init(*(ctypes.cast(getattr(_lib, f), ctypes.c_void_p).value for f in (
+        "entro_quantize_tokens", "entro_matmul_i8", "entro_attention_prompt", "entro_kv_append", "entro_kv_read", "entro_kv_attend")))
+    return _binding
+
+
 _lib = _load()
-# The usual calls of the operators around the coded weights, checked and made without the interpreter's part: each
-# returns None for anything that is not the plain valid case, and the function here goes on.
-_fast.init(*(ctypes.cast(getattr(_lib, f), ctypes.c_void_p).value for f in (
-    "entro_quantize_tokens", "entro_matmul_i8", "entro_attention_prompt", "entro_kv_append", "entro_kv_read", "entro_kv_attend")))
+_fast = _load_binding()
 
 
 def lib() -> ctypes.CDLL:
@@ -380,8 +399,8 @@ _TYPES = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16, torch.ui
 
 
 # The current device and its current stream's handle, without the objects that the public calls make of them.
-_current_device = torch._C._cuda_getDevice
-_current_stream = torch._C._cuda_getCurrentRawStream
+_current_device = getattr(torch._C, "_cuda_getDevice", None)  # (a build of torch without CUDA has neither, and no tensors for them)
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 class _on:

@@ -48,8 +48,18 @@ def _binding_command(target: str):
             "-lc10_cuda", "-lc10"]
 
 
+def _binding_wanted() -> bool:
+    """A build of torch without CUDA has nothing to link the module with, and no tensors to call it with."""
+    import torch
+    return torch.version.cuda is not None
+
+
+def _binding_stale() -> bool:
+    return _stale(BINDING, [BINDING_SOURCE, os.path.join(ROOT, "include", "entro.h")])
+
+
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
-    lib, binding = force or _stale(LIB, SOURCES + HEADERS), force or _stale(BINDING, [BINDING_SOURCE, os.path.join(ROOT, "include", "entro.h")])
+    lib, binding = force or _stale(LIB, SOURCES + HEADERS), _binding_wanted() and (force or _binding_stale())
     if not lib and not binding:
         return LIB
     os.makedirs(OBJECTS, exist_ok=True)
