@@ -20,6 +20,7 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libentro.so")
 OBJECTS = os.path.join(HERE, "_build")
 BINDING = os.path.join(HERE, "_binding.so")
+BINDING_MADE_FOR = os.path.join(OBJECTS, "binding_made_for.txt")
 BINDING_SOURCE = os.path.join(CSRC, "binding.cpp")
 SOURCES = [os.path.join(CSRC, f) for f in ("decode.cu", "product.cu", "prompt.cu", "kvcache.cu", "encoder.cpp", "launch.cpp")]
 HEADERS = sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".h", ".cuh"))) + [
@@ -54,8 +55,21 @@ def _binding_wanted() -> bool:
     return torch.version.cuda is not None
 
 
+def _binding_abi() -> str:
+    """What the module is bound to besides its source: torch's C++ interface and the interpreter's."""
+    import sysconfig
+
+    import torch
+    return f"torch {torch.__version__}, {sysconfig.get_config_var('SOABI')}"
+
+
 def _binding_stale() -> bool:
-    return _stale(BINDING, [BINDING_SOURCE, os.path.join(ROOT, "include", "entro.h")])
+    try:
+        with open(BINDING_MADE_FOR) as f:
+            made_for = f.read()
+    except FileNotFoundError:
+        return True
+    return made_for != _binding_abi() or _stale(BINDING, [BINDING_SOURCE, os.path.join(ROOT, "include", "entro.h")])
 
 
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
@@ -84,6 +98,9 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
             bad = bad or (p.returncode, cmd)
         else:
             os.replace(tmp, obj)
+            if obj == BINDING:
+                with open(BINDING_MADE_FOR, "w") as f:
+                    f.write(_binding_abi())
     if bad:
         raise subprocess.CalledProcessError(*bad)
     if not lib:

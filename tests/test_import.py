@@ -1,4 +1,5 @@
 """What importing the package needs: the library, the binding's module, and CUDA in torch only for the device side."""
+import importlib.util
 import os
 import pathlib
 import shutil
@@ -53,3 +54,25 @@ print("good")
 def test_the_host_side_needs_no_cuda_in_torch(tmp_path):
     code, out, err = _import(tmp_path, ("_binding.so",), _HOST_ONLY)
     assert code == 0 and out.strip() == "good", err[-2000:]
+
+
+def test_another_torch_or_interpreter_builds_the_binding_again(tmp_path, monkeypatch):
+    spec = importlib.util.spec_from_file_location("_builder_under_test", PACKAGE / "build.py")
+    builder = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(builder)
+    import sysconfig
+
+    import torch
+    made_for = tmp_path / "made_for.txt"
+    monkeypatch.setattr(builder, "BINDING_MADE_FOR", str(made_for))
+    monkeypatch.setattr(builder, "_stale", lambda *a: False)  # by its sources the module is up to date
+    assert builder._binding_stale()
+    made_for.write_text(builder._binding_abi())
+    assert not builder._binding_stale()
+    with monkeypatch.context() as m:
+        m.setattr(torch, "__version__", "0.0.1")
+        assert builder._binding_stale()
+    with monkeypatch.context() as m:
+        m.setattr(sysconfig, "get_config_var", lambda name: "cpython-399-x86_64-linux-gnu")
+        assert builder._binding_stale()
+    assert not builder._binding_stale()
