@@ -17,6 +17,7 @@ storage of "LazyWeights: Decode-on-Demand Edge LLMs" (arXiv 2611.17108v1).
 from __future__ import annotations
 
 import ctypes
+import operator
 import os
 from typing import List, NamedTuple, Optional, Sequence, Union
 
@@ -500,8 +501,13 @@ def matmul_i8(x: QuantTokens, w: torch.Tensor, w_scale: Union[float, torch.Tenso
         _vector(w_zero, "w_zero", torch.int32, rows, "[rows]")
     elif w_zero is None:
         w_zero = 0
-    elif not -2 ** 31 <= w_zero < 2 ** 31:
-        raise ValueError("w_zero must fit 32 bits")
+    else:
+        try:
+            w_zero = operator.index(w_zero)
+        except TypeError:
+            raise ValueError("w_zero must be a whole number, an int32 [rows] tensor or None") from None
+        if not -2 ** 31 <= w_zero < 2 ** 31:
+            raise ValueError("w_zero must fit 32 bits")
     index = w.get_device()
     _check_inputs(index, (w, q, scale, total, w_scale if ws else None, w_zero if wz else None, out, status),
                   ("w", "x.codes", "x.scale", "x.sum", "w_scale", "w_zero", "out", "status"))
@@ -524,7 +530,7 @@ def matmul_i8(x: QuantTokens, w: torch.Tensor, w_scale: Union[float, torch.Tenso
         raise ValueError("out must be fp32, bf16 or fp16")
     _check(_lib.entro_matmul_i8(qp, ldq, scale.data_ptr(), total.data_ptr(), tokens, wp, _TYPES[w.dtype], ldw, rows, cols,
                                 w_scale.data_ptr() if ws else None, 0.0 if ws else float(w_scale), w_zero.data_ptr() if wz else None,
-                                0 if wz else int(w_zero), out.data_ptr(), _TYPES[out.dtype], ldy,
+                                0 if wz else w_zero, out.data_ptr(), _TYPES[out.dtype], ldy,
                                 None if status is None else status.data_ptr(), _current_stream(index)), "entro_matmul_i8")
     return out
 
