@@ -566,7 +566,7 @@ def attention_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqle
     fp16 (slices of one projection's output as they are).  cu_seqlens int32 [batch + 1] says where each sequence's queries
     begin, cu_keys its keys (None: as the queries); a sequence's last query sees its last key, so queries that continue a
     context give their keys with it.  scale: 1 / sqrt(head_dim) by default.  Rows of no sequence are left as they are (give
-    `out` to keep theirs)."""
+    `out`, a tensor of its own, to keep theirs)."""
     if stream is None and out is None:
         done = _fast.attention_prompt(q, k, v, cu_seqlens, cu_keys, scale, status)
         if done is not None:
@@ -597,6 +597,8 @@ def attention_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqle
         os_ = _rows(out, "out", dtype, heads, dim, written=True)
         if out.shape[0] != tokens:
             raise ValueError("out must have q's shape")
+        if tokens and out.data_ptr() in (q.data_ptr(), k.data_ptr(), v.data_ptr()):
+            raise ValueError("out must not be q, k or v: they are read while it is written")
     scale = dim ** -0.5 if scale is None else float(scale)
     if not 0.0 < scale <= 2e38:
         raise ValueError("scale must be above 0 and finite")
