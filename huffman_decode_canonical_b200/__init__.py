@@ -57,6 +57,11 @@ class _KVCache(ctypes.Structure):
                 ("page_tokens", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("type", ctypes.c_int32)]
 
 
+class _ProductPlan(ctypes.Structure):
+    _fields_ = [("wide", ctypes.c_int32), ("tile_tokens", ctypes.c_int32), ("split", ctypes.c_int32), ("stages", ctypes.c_int32),
+                ("row_tiles", ctypes.c_int64), ("token_tiles", ctypes.c_int64)]
+
+
 class _Info(ctypes.Structure):
     _fields_ = [("bits", ctypes.c_int32), ("scheme", ctypes.c_int32), ("max_len", ctypes.c_int32),
                 ("format", ctypes.c_int32), ("rows", ctypes.c_int64), ("cols", ctypes.c_int64),
@@ -71,7 +76,7 @@ EXPORTS = ["entro_encode", "entro_blob_from_bytes", "entro_blob_bytes", "entro_b
            "entro_device_bytes", "entro_upload", "entro_tensor_free", "entro_decode_codes",
            "entro_decode_dequant_bf16", "entro_decode_gemv", "entro_group_table_bytes", "entro_group_prepare",
            "entro_group_launch", "entro_group_free", "entro_strerror", "entro_version", "entro_last_cuda_error",
-           "entro_decode_gemv_group_static", "entro_set_overlap", "entro_test_stall_tables",
+           "entro_decode_gemv_group_static", "entro_set_overlap", "entro_test_stall_tables", "entro_test_product_plan",
            "entro_quantize_tokens", "entro_unpack_codes", "entro_matmul_i8",
            "entro_kv_append", "entro_kv_read", "entro_kv_attend_workspace", "entro_kv_attend", "entro_attention_prompt"]
 
@@ -110,6 +115,7 @@ def _load() -> ctypes.CDLL:
         "entro_decode_gemv_group_static": ([P, P, P, I32, I32, P, P], I32),
         "entro_set_overlap": ([I32], I32),
         "entro_test_stall_tables": ([ctypes.c_uint32], ctypes.c_uint32),
+        "entro_test_product_plan": ([I64, I64, I64, I32, P], I32),
         "entro_kv_append": ([P, P, I64, I64, P, I64, I64, I64, P, P, I64, I32, P, P, I32, P, P], I32),
         "entro_kv_read": ([P, P, I64, I64, P, I64, I64, I64, P, P, I64, I32, P, I32, P, P], I32),
         "entro_kv_attend_workspace": ([P, ctypes.POINTER(U64)], I32),
@@ -791,6 +797,13 @@ def test_stall_tables(extra_bytes: int) -> int:
     return int(_lib.entro_test_stall_tables(int(extra_bytes)))
 
 
+def test_product_plan(tokens: int, rows: int, cols: int, sms: int = 148) -> dict:
+    """Test hook: how `matmul_i8` takes a call of these sizes on a device of `sms` SMs (`entro_test_product_plan`)."""
+    plan = _ProductPlan()
+    _check(_lib.entro_test_product_plan(tokens, rows, cols, sms, ctypes.byref(plan)), "entro_test_product_plan")
+    return {f: getattr(plan, f) for f, _ in _ProductPlan._fields_}
+
+
 def version() -> int:
     return int(_lib.entro_version())
 
@@ -806,6 +819,6 @@ def set_overlap(enable: bool) -> bool:
 
 __all__ = ["Blob", "DeviceTensor", "Group", "EntroError", "encode", "upload", "lib", "version", "set_overlap", "EXPORTS",
            "decode_gemv_group_static", "STATIC_GROUP_MAX", "QuantTokens", "quantize_tokens", "matmul_i8", "attention_prompt", "KVCache",
-           "test_stall_tables", "QUANT_AUTO", "QUANT_UNSIGNED", "QUANT_ASYM", "FORMAT_SINGLE", "FORMAT_LANES", "FORMAT_ROWS_CO",
+           "test_stall_tables", "test_product_plan", "QUANT_AUTO", "QUANT_UNSIGNED", "QUANT_ASYM", "FORMAT_SINGLE", "FORMAT_LANES", "FORMAT_ROWS_CO",
            "FORMAT_ROWS", "GROUP_GEMV",
            "GROUP_BF16", "SCHEME_UNSIGNED", "SCHEME_ASYM"]

@@ -539,6 +539,30 @@ static double narrow_cycles(int64_t row_tiles, int split, int sms, int chunks, i
     return static_cast<double>((ctas + sms - 1) / sms) * ((chunks + split - 1) / split) * step + 9000 + (split > 1 ? 60.0 * bn : 0.0);
 }
 
+// The kernel and the tile width whose waves cost least.
+static entro_product_plan plan_product(int64_t tokens, int64_t rows, int chunks, int sms) {
+    // wide tiles: pairs of SMs walk them
+    const int pairs = sms / 2;
+    const int64_t wide_rows = (rows + 255) / 256;
+    double wide_cost = 1e300;
+    int wide_bn = 256;
+    for (int bn = 256; bn >= 32; bn -= 32) {
+        const double c = wide_cycles((tokens + bn - 1) / bn * wide_rows, pairs, chunks, bn);
+        if (c < wide_cost) wide_cost = c, wide_bn = bn;
+    }
+    // one narrow tile of all tokens: k split as long as that fills SMs
+    const int narrow_bn = static_cast<int>(std::min<int64_t>((tokens + 15) / 16 * 16, 272));
+    const int64_t narrow_rows = (rows + kTileRows - 1) / kTileRows;
+    int split = 1;
+    while (split < 8 && split * 2 <= chunks && narrow_rows * split * 2 <= sms) split *= 2;
+    if (narrow_bn <= 256 && narrow_rows <= 65535 && narrow_cycles(narrow_rows, split, sms, chunks, narrow_bn) < wide_cost) {
+        const int stage = kABytes + narrow_bn * kChunkBytes;
+        return {0, narrow_bn, split, std::min(8, 100 * 1024 / stage < 3 ? 200 * 1024 / stage : 100 * 1024 / stage), narrow_rows, 1};
+    }
+    const int stage = kABytes + wide_bn / 2 * kChunkBytes;
+    return {1, wide_bn, 1, std::min(8, 200 * 1024 / stage), wide_rows, (tokens + wide_bn - 1) / wide_bn};
+}
+
 // 256 threads of up to four 16-byte loads; from 8192 columns on 512 (14336: 65 to 70 us, by 256 of eight loads 74 to 81).
 template <typename T>
 static const void *pick_quantize(int64_t cols, bool whole, unsigned *threads) {
@@ -618,30 +642,19 @@ extern "C" int entro_matmul_i8(const int8_t *d_q, int64_t ldq, const float *d_x_
     a.chunks = static_cast<int>((cols + kChunkBytes - 1) / kChunkBytes);
     a.tx_extra = test_tx_extra();
     const uint32_t types = kAccS32 | (w_type == ENTRO_S8 ? kAS8 : kAU8) | kBS8;
-    // wide tiles: the width whose waves cost least
-    const int pairs = di.sms / 2;
-    const int64_t wide_rows = (rows + 255) / 256;
-    double wide_cost = 1e300;
-    int wide_bn = 256;
-    for (int bn = 256; bn >= 32; bn -= 32) {
-        const double c = wide_cycles((tokens + bn - 1) / bn * wide_rows, pairs, a.chunks, bn);
-        if (c < wide_cost) wide_cost = c, wide_bn = bn;
-    }
-    // one narrow tile of all tokens: k split as long as that fills SMs
-    const int narrow_bn = static_cast<int>((tokens + 15) / 16 * 16);
-    const int64_t narrow_rows = (rows + kTileRows - 1) / kTileRows;
-    int split = 1;
-    while (split < 8 && split * 2 <= a.chunks && narrow_rows * split * 2 <= di.sms) split *= 2;
-    const bool narrow = narrow_bn <= 256 && narrow_rows <= 65535 && narrow_cycles(narrow_rows, split, di.sms, a.chunks, narrow_bn) < wide_cost;
+    const entro_product_plan plan = plan_product(tokens, rows, a.chunks, di.sms);
+    const bool narrow = !plan.wide;
+    a.bn = plan.tile_tokens;
+    a.stages = plan.stages;
+    if (plan.row_tiles * plan.token_tiles > INT32_MAX) return ENTRO_E_LIMIT;
+    a.row_tiles = static_cast<int>(plan.row_tiles);
+    a.token_tiles = static_cast<int>(plan.token_tiles);
     size_t smem;
     dim3 grid;
     unsigned cluster, threads;
     const void *fn;
     if (narrow) {
-        a.bn = narrow_bn;
-        a.row_tiles = static_cast<int>(narrow_rows);
-        const int stage = kABytes + a.bn * kChunkBytes;
-        a.stages = std::min(8, 100 * 1024 / stage < 3 ? 200 * 1024 / stage : 100 * 1024 / stage);
+        const int stage = kABytes + a.bn * kChunkBytes, split = plan.split;
         a.tmem_cols = 32;
         while (a.tmem_cols < static_cast<uint32_t>(a.bn)) a.tmem_cols *= 2;
         a.idesc = types | mma_shape(kTileRows, a.bn);
@@ -654,16 +667,10 @@ extern "C" int entro_matmul_i8(const int8_t *d_q, int64_t ldq, const float *d_x_
              : y_type == ENTRO_BF16 ? reinterpret_cast<const void *>(product_narrow_kernel<OUT_BF16T>)
                                     : reinterpret_cast<const void *>(product_narrow_kernel<OUT_F16T>);
     } else {
-        a.row_tiles = static_cast<int>(wide_rows);
-        a.bn = wide_bn;
-        a.token_tiles = static_cast<int>((tokens + a.bn - 1) / a.bn);
         const int stage = kABytes + a.bn / 2 * kChunkBytes;
-        a.stages = std::min(8, 200 * 1024 / stage);
         a.idesc = types | mma_shape(256, a.bn);
         smem = 1024 + static_cast<size_t>(a.stages) * stage;
-        const int64_t tiles = static_cast<int64_t>(a.row_tiles) * a.token_tiles;
-        if (tiles > INT32_MAX) return ENTRO_E_LIMIT;
-        grid = dim3(2 * static_cast<unsigned>(std::min<int64_t>(tiles, pairs)));
+        grid = dim3(2 * static_cast<unsigned>(std::min<int64_t>(plan.row_tiles * plan.token_tiles, di.sms / 2)));
         cluster = 1;  // the pair is the kernel's own cluster size
         threads = 256;
         fn = y_type == ENTRO_F32 ? reinterpret_cast<const void *>(product_wide_kernel<OUT_F32>)
@@ -683,4 +690,11 @@ extern "C" int entro_matmul_i8(const int8_t *d_q, int64_t ldq, const float *d_x_
     const bool early = static_cast<int64_t>(grid.x) * grid.y <= di.sms;
     e = launch_ex(fn, grid, threads, smem, static_cast<cudaStream_t>(stream), cluster, early, args);
     return e == cudaSuccess ? ENTRO_OK : cuda_fail(e, "entro_matmul_i8");
+}
+
+extern "C" int entro_test_product_plan(int64_t tokens, int64_t rows, int64_t cols, int32_t sms, entro_product_plan *plan) {
+    if (!plan || tokens < 1 || rows < 1 || cols < 1 || sms < 2) return ENTRO_E_INVAL;
+    if (tokens > ENTRO_PRODUCT_MAX_TOKENS || cols > ENTRO_PRODUCT_MAX_COLS || rows > (INT64_C(1) << 30)) return ENTRO_E_LIMIT;
+    *plan = plan_product(tokens, rows, static_cast<int>((cols + kChunkBytes - 1) / kChunkBytes), sms);
+    return ENTRO_OK;
 }

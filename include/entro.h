@@ -387,6 +387,17 @@ ENTRO_API int entro_set_overlap(int enable);
  * default) turns it off.  Process-wide; returns the previous value. */
 ENTRO_API uint32_t entro_test_stall_tables(uint32_t extra_bytes);
 
+/* Test hook: how entro_matmul_i8 takes a call of these sizes on a device of `sms`
+ * SMs (the cost model alone; needs no GPU).  wide 0: a cluster of `split` CTAs
+ * shares the columns of each tile of 128 weight rows by tile_tokens (all) tokens;
+ * wide 1: sms / 2 pairs of CTAs walk the tiles of 256 rows by tile_tokens tokens.
+ * `stages` steps of 128 columns are in flight. */
+typedef struct entro_product_plan {
+    int32_t wide, tile_tokens, split, stages;
+    int64_t row_tiles, token_tiles;
+} entro_product_plan;
+ENTRO_API int entro_test_product_plan(int64_t tokens, int64_t rows, int64_t cols, int32_t sms, entro_product_plan *plan);
+
 /* Text of the last CUDA runtime error behind an ENTRO_E_CUDA return on the
  * calling host thread ("" if none). */
 ENTRO_API const char *entro_last_cuda_error(void);
