@@ -269,9 +269,10 @@ __device__ __forceinline__ void join_parts(const PromptArgs &a, const PromptItem
     const int end = min(row0 + share, rows);
     uint32_t odd = 0;
     for (int p = 0; p < parts; p++) {
-        uint32_t x;
+        uint32_t x, y;
         asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(x) : "r"(map_to(special, p)) : "memory");
-        odd |= x;
+        asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(y) : "r"(map_to(special + 16, p)) : "memory");
+        odd |= x | y;
     }
     if (odd) {
         for (int r = row0 + warp; r < end; r += 8)
@@ -323,7 +324,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     __shared__ PromptItem items[2];
     __shared__ __align__(8) uint64_t bars[2 * kStages + 23 + 2 * kMarks];
     __shared__ uint32_t tmem_base;
-    __shared__ int failed, special[4];
+    __shared__ int failed, special[8];  // per query tile: items with values that are not finite (item n in place n % 4)
     const uint32_t base = (smem_u32(smem_raw) + 1023) & ~1023u, ring = base + 2 * Shape::kQTile;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     // Barriers, each with a count of its own that goes on from item to item:
@@ -360,7 +361,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                 bar_init(v_seen + 8 * j, 1);
             }
             fence_bar_init();
-            failed = special[0] = special[1] = special[2] = special[3] = 0;
+            failed = 0;
+            for (int x = 0; x < 8; x++) special[x] = 0;
         }
     } else if (warp == 1 && lane == 0) {
         prefetch_map(&q_map);
@@ -456,7 +458,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             PromptItem it;
             int i = 0, g = 0;
             for (int n_item = 0; ok && take(n_item, it); n_item++) {
-                const int n = max(it.key_tiles<kKeys>(0), it.key_tiles<kKeys>(1));
+                const int n0 = it.key_tiles<kKeys>(0), n1 = it.key_tiles<kKeys>(1), n = max(n0, n1);
                 for (int j = it.masked_from<kKeys>(); j < n; j++, g++) {
                     const int iv = i + 2 * j + 1;
                     if (!__all_sync(~0u, bar_wait(v_sent + 8 * (g % kMarks), g / kMarks & 1) && bar_wait(full + 8 * (iv % kStages), iv / kStages & 1))) {
@@ -484,7 +486,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                         for (int u = there * 8 + lane; u < kKeys * 8; u += 32)
                             asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(chunk + u * 16), "r"(0) : "memory");
                     }
-                    if (odd & 0x80008000u) special[n_item % 4] = n_item + 1;  // (at most two items ahead of a softmax warp)
+                    // For each query tile that these values are multiplied with, and no other: that one's softmax warps may
+                    // be past this item.  (At most two items ahead of a softmax warp.)
+                    if (odd & 0x80008000u) {
+                        if (j < n0) special[n_item % 4] = n_item + 1;
+                        if (j < n1) special[4 + n_item % 4] = n_item + 1;
+                    }
                     fence_async_smem();
                     __syncwarp();
                     if (lane == 0) bar_arrive(v_seen + 8 * (g % kMarks));
@@ -676,7 +683,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                 __syncwarp();
                 if (lane == 0) bar_arrive(o_empty + 8 * t);
                 // (this tile's values have all been looked over before its output was complete)
-                if (*static_cast<volatile int *>(&special[n_item % 4]) == n_item + 1)
+                if (*static_cast<volatile int *>(&special[t * 4 + n_item % 4]) == n_item + 1)
                     for (int r = it.row0 + warp * 32; r < min(it.row0 + warp * 32 + 32, it.qlen); r++)
                         row_by_row<T, D>(a, it.head, static_cast<int64_t>(it.q0) + r, it.k0, max(r + it.offset + 1, 0));
             }
