@@ -122,46 +122,46 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs
     const bool ok = page >= 0 && page < a.c.pages;
     if (!ok) set_status(a.status, ENTRO_E_INVAL);
     for (int h = blockIdx.y * a.heads; h < min((blockIdx.y + 1) * a.heads, static_cast<unsigned>(a.c.kv)); h++) {
-    T *tail = static_cast<T *>(a.c.tail[kind]) + (static_cast<int64_t>(slot) * a.c.kv + h) * (P * D);
-    const T *in = static_cast<const T *>(a.in[kind]) + begin * a.in_token[kind] + h * a.in_head[kind];
-    if (block != last_open) {
-        uint4 v[kMine];
-        uint32_t m = 0;
-#pragma unroll
-        for (int i = 0; i < kMine; i++) {
-            const int u = i * kAppendThreads + tid;
-            if (kVecs % kAppendThreads && u >= kVecs) break;
-            const int t = u / kRow, x = u % kRow * 8, pos = block * P + t;
-            v[i] = *reinterpret_cast<const uint4 *>(pos < start ? tail + t * D + x : in + (pos - start) * a.in_token[kind] + x);
-            m = __vmaxu2(m, __vmaxu2(__vmaxu2(v[i].x & 0x7FFF7FFFu, v[i].y & 0x7FFF7FFFu),
-                                     __vmaxu2(v[i].z & 0x7FFF7FFFu, v[i].w & 0x7FFF7FFFu)));
-        }
-        m = __reduce_max_sync(~0u, max(m & 0xFFFF, m >> 16));
-        if (tid % 32 == 0) red[tid / 32] = m;
-        __syncthreads();
-#pragma unroll
-        for (int w = 0; w < kAppendThreads / 32; w++) m = max(m, red[w]);
-        const BlockCode<T> code(m);
-        int8_t *out = a.c.codes[kind] + (static_cast<int64_t>(ok ? page : 0) * a.c.kv + h) * (P * D);
-        if (ok) {
+        T *tail = static_cast<T *>(a.c.tail[kind]) + (static_cast<int64_t>(slot) * a.c.kv + h) * (P * D);
+        const T *in = static_cast<const T *>(a.in[kind]) + begin * a.in_token[kind] + h * a.in_head[kind];
+        if (block != last_open) {
+            uint4 v[kMine];
+            uint32_t m = 0;
 #pragma unroll
             for (int i = 0; i < kMine; i++) {
                 const int u = i * kAppendThreads + tid;
                 if (kVecs % kAppendThreads && u >= kVecs) break;
-                *reinterpret_cast<uint2 *>(out + u * 8) = code.eight(v[i]);
+                const int t = u / kRow, x = u % kRow * 8, pos = block * P + t;
+                v[i] = *reinterpret_cast<const uint4 *>(pos < start ? tail + t * D + x : in + (pos - start) * a.in_token[kind] + x);
+                m = __vmaxu2(m, __vmaxu2(__vmaxu2(v[i].x & 0x7FFF7FFFu, v[i].y & 0x7FFF7FFFu),
+                                         __vmaxu2(v[i].z & 0x7FFF7FFFu, v[i].w & 0x7FFF7FFFu)));
             }
-            if (tid == 0) a.c.scale[kind][static_cast<int64_t>(page) * a.c.kv + h] = code.scale();
+            m = __reduce_max_sync(~0u, max(m & 0xFFFF, m >> 16));
+            if (tid % 32 == 0) red[tid / 32] = m;
+            __syncthreads();
+#pragma unroll
+            for (int w = 0; w < kAppendThreads / 32; w++) m = max(m, red[w]);
+            const BlockCode<T> code(m);
+            int8_t *out = a.c.codes[kind] + (static_cast<int64_t>(ok ? page : 0) * a.c.kv + h) * (P * D);
+            if (ok) {
+#pragma unroll
+                for (int i = 0; i < kMine; i++) {
+                    const int u = i * kAppendThreads + tid;
+                    if (kVecs % kAppendThreads && u >= kVecs) break;
+                    *reinterpret_cast<uint2 *>(out + u * 8) = code.eight(v[i]);
+                }
+                if (tid == 0) a.c.scale[kind][static_cast<int64_t>(page) * a.c.kv + h] = code.scale();
+            }
+            __syncthreads();  // the older tokens have been read (and the maxima)
+            if (block != first || !older || last_open < 0) continue;
         }
-        __syncthreads();  // the older tokens have been read (and the maxima)
-        if (block != first || !older || last_open < 0) continue;
-    }
-    // the open block's new tokens into the tail
-    const int from = max(start, last_open * P);
-    for (int u = tid; u < (end - from) * kRow; u += kAppendThreads) {
-        const int pos = from + u / kRow, x = u % kRow * 8;
-        *reinterpret_cast<uint4 *>(tail + pos % P * D + x) =
-            __ldg(reinterpret_cast<const uint4 *>(in + (pos - start) * a.in_token[kind] + x));
-    }
+        // the open block's new tokens into the tail
+        const int from = max(start, last_open * P);
+        for (int u = tid; u < (end - from) * kRow; u += kAppendThreads) {
+            const int pos = from + u / kRow, x = u % kRow * 8;
+            *reinterpret_cast<uint4 *>(tail + pos % P * D + x) =
+                __ldg(reinterpret_cast<const uint4 *>(in + (pos - start) * a.in_token[kind] + x));
+        }
     }
 }
 
@@ -394,8 +394,7 @@ struct StepLayout {
     }
     static __device__ __forceinline__ uint32_t value(int row, int byte) {
         if (D == 96) return row * D + byte;
-        const int at = row * D + byte, line = D == 128 ? row / 2 : row / 2;  // (rows 2 tig: a line of 128 bytes each, or two)
-        return at ^ ((line & 3) * 32);
+        return (row * D + byte) ^ ((row / 2 & 3) * 32);  // (rows 2 tig: a line of 128 bytes each, or two)
     }
 };
 template <int N>
@@ -405,24 +404,22 @@ __device__ __forceinline__ void load_shared(uint32_t *r, uint32_t at) {
     else asm volatile("ld.shared.u32 %0, [%1];" : "=r"(r[0]) : "r"(at));
 }
 
-// N bytes (8, 12, 16, 24 or 32) from an address aligned to the largest power of two in N
+// N bytes (16, 24, 32, 48 or 64) from an address aligned to the largest power of two in N, up to 16
 template <int N>
 __device__ __forceinline__ void load_bytes(uint32_t *r, const void *p) {
+    static_assert(N % 8 == 0, "");
     if (N % 16 == 0) {
 #pragma unroll
         for (int i = 0; i < N / 16; i++) {
             const uint4 v = __ldg(static_cast<const uint4 *>(p) + i);
             r[4 * i] = v.x, r[4 * i + 1] = v.y, r[4 * i + 2] = v.z, r[4 * i + 3] = v.w;
         }
-    } else if (N % 8 == 0) {
+    } else {
 #pragma unroll
         for (int i = 0; i < N / 8; i++) {
             const uint2 v = __ldg(static_cast<const uint2 *>(p) + i);
             r[2 * i] = v.x, r[2 * i + 1] = v.y;
         }
-    } else {
-#pragma unroll
-        for (int i = 0; i < N / 4; i++) r[i] = __ldg(static_cast<const uint32_t *>(p) + i);
     }
 }
 // A power of two that brings numbers of at most this magnitude (the bits of a
@@ -530,12 +527,6 @@ struct Weights16 {
         : p0(transpose8x8(Half<__half>::pack(e[0], e[1]))), p1(transpose8x8(Half<__half>::pack(e[2], e[3]))) {}
 };
 
-// One pass over the cache.  A CTA's share of all tiles is one row of tiles, cut
-// where the (sequence, head) changes; a piece that covers all of its sequence and
-// head is finished here, others leave (m, l, o) behind for the join.  Bound by
-// reading the codes, 2 D bytes of a token and key head: 48 sequences of up to 16000
-// tokens, 8 key heads of 128: 183 us, 5.75 TB/s; of up to 2500 with 32 key heads of 96,
-// where pieces are short: 99 us, 4.8 TB/s; one of 1000 tokens: 7.9 us with the join.
 // A warp's steps in flight, the one at work among them.  Two with 16 warps on an SM keep memory as busy as it gets
 // (48 sequences of 16000 tokens, 8 key heads of 128: 191 us; three 199, four 227).
 constexpr int kSteps = 2;
@@ -546,6 +537,12 @@ constexpr int attend_smem() {
     return steps > join ? steps : join;
 }
 
+// One pass over the cache.  A CTA's share of all tiles is one row of tiles, cut
+// where the (sequence, head) changes; a piece that covers all of its sequence and
+// head is finished here, others leave (m, l, o) behind for the join.  Bound by
+// reading the codes, 2 D bytes of a token and key head: 48 sequences of up to 16000
+// tokens, 8 key heads of 128: 183 us, 5.75 TB/s; of up to 2500 with 32 key heads of 96,
+// where pieces are short: 99 us, 4.8 TB/s; one of 1000 tokens: 7.9 us with the join.
 template <typename T, int D>
 __global__ void __launch_bounds__(kAttendThreads, 4) attend_kernel(const AttendArgs a) {
     using Layout = StepLayout<D>;

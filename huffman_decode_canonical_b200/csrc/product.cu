@@ -601,9 +601,15 @@ extern "C" int entro_unpack_codes(const void *d_codes, int32_t bits, int64_t row
     const int64_t words = rows * (ld / 16);
     const uint8_t *codes = static_cast<const uint8_t *>(d_codes);
     uint8_t *out = static_cast<uint8_t *>(d_out);
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+    DeviceInfo di;
+    const int r = device_info(dev, &di);
+    if (r != ENTRO_OK) return r;
     void *args[] = {&codes, &bits, &rows, &cols, &out, &ld};
-    cudaError_t e = launch_ex(reinterpret_cast<const void *>(unpack_kernel), dim3(static_cast<unsigned>(std::min<int64_t>((words + 255) / 256, 148 * 16))),
-                              256, 0, static_cast<cudaStream_t>(stream), 1, false, args);
+    e = launch_ex(reinterpret_cast<const void *>(unpack_kernel), dim3(static_cast<unsigned>(std::min<int64_t>((words + 255) / 256, di.sms * 16))),
+                  256, 0, static_cast<cudaStream_t>(stream), 1, false, args);
     return e == cudaSuccess ? ENTRO_OK : cuda_fail(e, "entro_unpack_codes");
 }
 
