@@ -428,9 +428,11 @@ class _on:
 
 def _check_inputs(index: int, tensors, names):
     """Refuses what the kernels must not be given: tensors of other devices, or ones that ask for gradients (backward or
-    forward: a tangent would be lost); a status that is no int32 word (the last one named so)."""
+    forward: a tangent would be lost); a status that is no int32 word (the last one named so); any call of a trace."""
     if index < 0:
         raise ValueError("expected CUDA tensors")
+    if torch.jit.is_tracing():
+        raise ValueError("this call cannot be traced: its result would be a constant of the trace")
     if names[-1] == "status" and tensors[-1] is not None and (tensors[-1].dtype is not torch.int32 or tensors[-1].numel() < 1):
         raise ValueError("status must be an int32 tensor")
     grad = torch.is_grad_enabled()

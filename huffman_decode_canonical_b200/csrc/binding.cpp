@@ -11,6 +11,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/TracerMode.h>
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/core/GradMode.h>
 #include <c10/cuda/CUDAFunctions.h>
@@ -74,7 +75,8 @@ bool half_type(ScalarType t) { return t == ScalarType::BFloat16 || t == ScalarTy
 Tensor make(c10::IntArrayRef size, ScalarType type, int index) {
     return at::detail::empty_cuda(size, type, c10::Device(c10::kCUDA, static_cast<c10::DeviceIndex>(index)), std::nullopt);
 }
-bool here(int index) { return c10::cuda::current_device() == index; }
+// The current device, and no trace being taken: a call's result would be a constant of it.
+bool here(int index) { return c10::cuda::current_device() == index && !at::tracer::impl::is_dispatch_enabled(); }
 void *stream(int index) { return c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(index)).stream(); }
 
 // [tokens, heads, dim] in 16-byte pieces: token and head stride (0 where there is one)
