@@ -274,7 +274,9 @@ constexpr int kAttendThreads = 128;
 constexpr int kTile = 64;         // tokens a CTA takes at a time, 16 a warp
 constexpr int kHeads = 8;         // query heads of an MMA
 constexpr float kLazy = 8.0f;     // the reference maximum is raised when a score passes it by 2^8
-constexpr float kBias = 6.0f;     // weights are held as 2^6 times theirs: at most 2^14 in 16 bits, 2^-30 at least
+// Weights are held as 2^6 times theirs, at most 2^14, in fp16: off by 2^-11 of themselves, or by 2^-31 where that is more.
+// (Their products with the codes are exact in fp16 alone: a bfloat16 weight would be off by 2^-8.)
+constexpr float kBias = 6.0f;
 
 // The cached length, cut to the table's pages and an open block (both kernels agree on it).
 __device__ __forceinline__ int clean_len(const AttendArgs &a, int b, bool report) {
@@ -528,7 +530,7 @@ struct Weights16 {
 };
 
 // A warp's steps in flight, the one at work among them.  Two with 16 warps on an SM keep memory as busy as it gets
-// (48 sequences of 16000 tokens, 8 key heads of 128: 191 us; three 199, four 227).
+// (48 sequences of 8192 to 32768 tokens, 8 key heads of 128: 391 us; three 425, four 474, in turns).
 constexpr int kSteps = 2;
 
 template <int D>
@@ -540,9 +542,9 @@ constexpr int attend_smem() {
 // One pass over the cache.  A CTA's share of all tiles is one row of tiles, cut
 // where the (sequence, head) changes; a piece that covers all of its sequence and
 // head is finished here, others leave (m, l, o) behind for the join.  Bound by
-// reading the codes, 2 D bytes of a token and key head: 48 sequences of up to 16000
-// tokens, 8 key heads of 128: 183 us, 5.75 TB/s; of up to 2500 with 32 key heads of 96,
-// where pieces are short: 99 us, 4.8 TB/s; one of 1000 tokens: 7.9 us with the join.
+// reading the codes, 2 D bytes of a token and key head: 48 sequences of 8192 to 32768
+// tokens, 8 key heads of 128: 391 to 422 us from run to run, 5.0 to 5.4 TB/s; of 625 to 2500 with 32 key heads of 96, where pieces are short: 97 us, 4.5
+// TB/s; one of 1000 tokens: 8.2 us with the join, in a graph.
 template <typename T, int D>
 __global__ void __launch_bounds__(kAttendThreads, 4) attend_kernel(const AttendArgs a) {
     using Layout = StepLayout<D>;

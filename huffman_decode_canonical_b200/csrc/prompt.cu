@@ -13,13 +13,19 @@
 // it by 2^8 (any reference gives the same quotient), so O is rarely rescaled.
 // Bound by the exponentials and the MMAs about alike at 128 channels (128 x 128
 // scores take 16384 exponentials, 16 a clock and SM, and 2 x 128 x 128 x D
-// multiply-adds, 4096 a clock), by the exponentials and the instructions around
-// them at 64 and 96.  8192 tokens, 32 heads of 128 over 8: 430 us in a short run (1280
-// TFLOP/s), about 510 in a long one at the power limit; 4096 tokens, 32 heads of 64: 106
-// to 122 us (563 to 649, from run to run); 5 prompts of 6011 tokens in all, 32 heads of 96: 97 us (688).  Taking a part of
+// multiply-adds, 4096 a clock).  8192 tokens, 32 heads of 128 over 8: 441 us in a row of
+// 9 calls (1248 TFLOP/s), 510 in a long one, at the power limit.  At 64 and 96 the
+// exponentials take longer than the MMAs, but neither accounts for the time: 4096 tokens,
+// 32 heads of 64: 108 us (640); 6011 tokens, 32 heads of 96: 277 to 294 us (755 to 802),
+// in 5 prompts of uneven lengths 127 to 130 (600).  Taking a part of
 // the exponentials by a polynomial instead, looking for the maximum only after a weight
 // came out too large, or fetching the next scores beside the exponentials was slower (in
 // an earlier form 463 us -> 489 to 518, 562, and 510).
+//
+// The weights are rounded to the inputs' type (half a step of it, of each weight): both
+// operands of an MMA have one type, and values in bfloat16 do not fit fp16.  A second
+// product with the weights' remainders would add half of the MMAs again.  The sums of
+// the weights take them as they were in 32 bits.
 //
 // Few queries over many keys leave most SMs without a block: there a cluster of up
 // to eight CTAs shares the keys of a block (see join_parts).

@@ -223,10 +223,12 @@ ENTRO_API int entro_decode_gemv_group_static(const entro_tensor *const *tensors,
  * besides single tokens' products -- products of a whole prompt, attention
  * over the prompt, and attention over an 8-bit key/value cache.  Not on the
  * EntroLLM or LazyWeights pages.  The calls below run on the current device,
- * which must be the one that holds their buffers.  Their kernels are launched
- * so that they may start while the kernel before them on the stream finishes;
- * they touch memory only after it has completed.  Nothing is allocated, on the
- * host heap or on the device, and all calls may be captured into graphs.
+ * which must be the one that holds their buffers.  The product, and the join
+ * that ends an attention over the cache of few heads, are launched so that they
+ * may start while the kernel before them on the stream finishes; they touch
+ * memory that a kernel writes only after that one has completed.  Nothing is
+ * allocated, on the host heap or on the device, and all calls may be captured
+ * into graphs.
  * Outputs must not overlap inputs.  A call whose waits give up (see
  * ENTRO_E_TIMEOUT) leaves its outputs incomplete.
  * ------------------------------------------------------------------------ */
@@ -351,8 +353,10 @@ ENTRO_API int entro_kv_read(const entro_kv_cache *cache, void *d_k, int64_t k_to
  *   out[b,h] = sum_j p_j v_j,  p = softmax_j(scale q[b,h] . k_j),  j < d_lens[b]
  * over the values that the cache stands for.  A sequence without tokens gets 0 (one
  * whose tokens all score -infinity NaN).
- * Scores, sums and outputs are taken in fp32, the weights p rounded to fp16; a
- * result does not depend on when it is computed (no atomics), but on the batch,
+ * Scores, sums and outputs are taken in fp32, the weights p rounded to fp16 (off
+ * by 2^-11 of themselves or 2^-31, whichever is more); sums of weights times
+ * values are held at up to 2^14 times theirs, so values from 2^113 on may overflow.
+ * A result does not depend on when it is computed (no atomics), but on the batch,
  * which decides how the work is split.  scale > 0.  d_work: device memory of at
  * least entro_kv_attend_workspace bytes, 16-byte aligned, of this call alone until
  * it has run. */
