@@ -354,9 +354,8 @@ ENTRO_API int entro_kv_read(const entro_kv_cache *cache, void *d_k, int64_t k_to
  * over the values that the cache stands for.  A sequence without tokens gets 0 (one
  * whose tokens all score -infinity NaN).
  * Scores, sums and outputs are taken in fp32, the weights p rounded to fp16 (off
- * by 2^-11 of themselves or 2^-31, whichever is more); sums of weights times
- * values are held at up to 2^14 times theirs, so values from 2^113 on may overflow.
- * A result does not depend on when it is computed (no atomics), but on the batch,
+ * by 2^-11 of themselves or 2^-31, whichever is more).  The sums of e^(s_j - max)
+ * v_j are held at up to 2^14 times theirs and may overflow from 2^114 on.  A result does not depend on when it is computed (no atomics), but on the batch,
  * which decides how the work is split.  scale > 0.  d_work: device memory of at
  * least entro_kv_attend_workspace bytes, 16-byte aligned, of this call alone until
  * it has run. */
