@@ -32,9 +32,10 @@
 //
 // What the mask hides must not count, whatever it holds.  Scores are replaced one
 // by one.  Values of a tile that some row must not see are looked over in shared
-// memory before their MMA: rows past the sequence's keys are zeroed, and where a
-// visible row holds an infinity or NaN (0 times it would reach rows that do not
-// see it) the CTA's rows are computed again one by one.
+// memory before their MMA: rows past the sequence's keys are zeroed, and so are
+// infinities and NaN (0 times one would reach rows that do not see it), which are
+// added to the outputs of the rows that do see them: a weight above 0 times an
+// infinity, and whatever is finite besides, is that infinity.
 #include <algorithm>
 #include <cstring>
 
@@ -93,52 +94,47 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return r;
 }
 
-// One row by the definition, by one warp: for rows whose tile holds an infinity
-// or NaN among values that other rows do not see.
+// Exponents of all ones, in either half of a word, carry into the sign bits.
+template <typename T>
+__device__ __forceinline__ uint32_t not_finite(uint32_t x) {
+    constexpr uint32_t kOne = Half<T>::kExp == 0x7C007C00u ? 0x04000400u : 0x00800080u;
+    return ((x & Half<T>::kExp) + kOne) & 0x80008000u;
+}
+
+// By a warp, a row a lane: the infinities and NaN among the values of keys [from, to) to the outputs (written before) of
+// the rows that see them, keys up to `last`.  A key that scores -infinity has weight 0, and 0 times them is NaN.  A block's
+// keys of this kind are some 320 at most (its queries' and the rest of a tile), so this takes no longer for a long context.
 template <typename T, int D>
-__device__ __forceinline__ void row_by_row(const PromptArgs &a, int head, int64_t q_row, int64_t k_row, int visible) {
+__device__ __forceinline__ void add_not_finite(const PromptArgs &a, int head, int64_t q_row, int64_t k_row, int from, int to, bool mine, int last) {
     const int lane = threadIdx.x % 32;
     const T *q = static_cast<const T *>(a.q) + q_row * a.q_token + head * a.q_head;
     const T *k = static_cast<const T *>(a.k) + k_row * a.k_token + (head / a.group) * a.k_head;
     const T *v = static_cast<const T *>(a.v) + k_row * a.v_token + (head / a.group) * a.v_head;
-    float m = -INFINITY, l = 0.0f, o[D / 32];
-#pragma unroll
-    for (int i = 0; i < D / 32; i++) o[i] = 0.0f;
-    for (int j0 = 0; j0 < visible; j0 += 32) {
-        float s = -INFINITY;
-        if (j0 + lane < visible) {
-            s = 0.0f;
-            const T *row = k + (j0 + lane) * a.k_token;
+    T *out = static_cast<T *>(a.out) + q_row * a.out_token + head * a.out_head;
+#pragma unroll 1
+    for (int j0 = from; j0 < to; j0 += 32) {
+        uint32_t odd = 0;
+        if (j0 + lane < to) {
+            const T *row = v + (j0 + lane) * a.v_token;
             for (int d = 0; d < D; d += 8) {
-                const uint4 x = *reinterpret_cast<const uint4 *>(row + d), y = *reinterpret_cast<const uint4 *>(q + d);
-                const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-                for (int i = 0; i < 4; i++) {
-                    const float2 f = Half<T>::widen(xs[i]), g = Half<T>::widen(ys[i]);
-                    s = fmaf(f.x, g.x, fmaf(f.y, g.y, s));
-                }
+                const uint4 x = *reinterpret_cast<const uint4 *>(row + d);
+                odd |= not_finite<T>(x.x) | not_finite<T>(x.y) | not_finite<T>(x.z) | not_finite<T>(x.w);
             }
-            s *= a.scale_log2;
         }
-        float n = fmaxf(m, s);
-        for (int x = 16; x; x /= 2) n = fmaxf(n, __shfl_xor_sync(~0u, n, x));
-        const float base = n == -INFINITY ? 0.0f : n;
-        const float f = m == n ? 1.0f : exp2_fast(m - base), p = exp2_fast(s - base);
-        m = n;
-        l = l * f + p;
-#pragma unroll
-        for (int i = 0; i < D / 32; i++) o[i] *= f;
-        for (int j = 0; j < 32 && j0 + j < visible; j++) {
-            const float w = __shfl_sync(~0u, p, j);
-            const T *row = v + (j0 + j) * a.v_token;
-#pragma unroll
-            for (int i = 0; i < D / 32; i++) o[i] = fmaf(w, static_cast<float>(row[i * 32 + lane]), o[i]);
+        for (uint32_t keys = __ballot_sync(~0u, odd != 0); keys; keys &= keys - 1) {
+            const int j = j0 + __ffs(keys) - 1;
+            if (!mine || j > last) continue;
+            float s = 0.0f;
+#pragma unroll 1
+            for (int d = 0; d < D; d++) s = fmaf(static_cast<float>(q[d]), static_cast<float>(k[j * a.k_token + d]), s);
+            const bool none = s * a.scale_log2 == -INFINITY;
+#pragma unroll 1
+            for (int d = 0; d < D; d++) {
+                const float x = static_cast<float>(v[j * a.v_token + d]);
+                if (!(fabsf(x) < INFINITY)) out[d] = static_cast<T>(static_cast<float>(out[d]) + (none ? __int_as_float(0x7FC00000) : x));
+            }
         }
     }
-    for (int x = 16; x; x /= 2) l += __shfl_xor_sync(~0u, l, x);
-    T *out = static_cast<T *>(a.out) + q_row * a.out_token + head * a.out_head;
-#pragma unroll
-    for (int i = 0; i < D / 32; i++) out[i * 32 + lane] = static_cast<T>(visible > 0 ? o[i] / l : 0.0f);
 }
 
 // What a CTA works on: 256 queries of a head.
@@ -164,6 +160,8 @@ struct PromptItem {
         const int n = max(key_tiles<KEYS>(0), key_tiles<KEYS>(1)), from = n * i / of * KEYS, to = min(n * (i + 1) / of * KEYS, klen);
         skipped = from, k0 += from, offset -= from, klen = max(to - from, 0);
     }
+    // back to the whole sequence's keys (but for their number)
+    __device__ __forceinline__ void join_cut() { k0 -= skipped, offset += skipped, skipped = 0; }
 };
 
 // Block number -> item, by a warp: heads fastest, so that those of a key head meet in L2; of a sequence's blocks the
@@ -243,7 +241,7 @@ __device__ __forceinline__ void skip_join() {
 // By the softmax warps, a row a thread: the parts go to their CTAs' shared memory, where queries, keys and values were
 // (nothing reads those any more when all warps are here), and each CTA finishes a share of the rows.
 template <typename T, int D>
-__device__ __forceinline__ void join_parts(const PromptArgs &a, const PromptItem it, uint32_t base, uint32_t ot, float m, float l, bool any,
+__device__ __forceinline__ void join_parts(const PromptArgs &a, PromptItem it, uint32_t base, uint32_t ot, float m, float l, bool any,
                                         uint32_t special) {
     const int tid = threadIdx.x, warp = tid / 32;
     const uint32_t stats = base + 256 * D * 4;
@@ -280,11 +278,7 @@ __device__ __forceinline__ void join_parts(const PromptArgs &a, const PromptItem
         asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(y) : "r"(map_to(special + 16, p)) : "memory");
         odd |= x | y;
     }
-    if (odd) {
-        for (int r = row0 + warp; r < end; r += 8)
-            row_by_row<T, D>(a, it.head, static_cast<int64_t>(it.q0) + it.row0 + r, it.k0 - it.skipped,
-                             max(it.row0 + r + it.offset + it.skipped + 1, 0));
-    } else {
+    {
         const float c = a.scale_log2;
         for (int u = tid; u < (end - row0) * (D / 8); u += 256) {
             const int r = row0 + u / (D / 8), d = u % (D / 8) * 2;  // 8 channels: pieces d and d + 1
@@ -312,6 +306,14 @@ __device__ __forceinline__ void join_parts(const PromptArgs &a, const PromptItem
             T *out = static_cast<T *>(a.out) + (static_cast<int64_t>(it.q0) + it.row0 + r) * a.out_token + it.head * a.out_head;
             *reinterpret_cast<uint4 *>(out + d * 4) = make_uint4(h[0], h[1], h[2], h[3]);
         }
+    }
+    if (odd) {  // (of the whole cluster: all warps agree)
+        asm volatile("barrier.sync 2, 256;" ::: "memory");
+        it.join_cut();
+        const int r = row0 + tid, top = min(row0 + warp * 32 + 31, end - 1);
+        if (row0 + warp * 32 < end)
+            add_not_finite<T, D>(a, it.head, static_cast<int64_t>(it.q0) + it.row0 + min(r, end - 1), it.k0, it.masked_from<PromptShape<D>::kKeys>() * PromptShape<D>::kKeys,
+                                 it.row0 + top + it.offset + 1, r < end, it.row0 + r + it.offset);
     }
     __syncwarp();
     cluster_sync();  // the others have read this CTA's part
@@ -473,9 +475,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                     }
                     const uint32_t tile = ring + iv % kStages * Shape::kTile;
                     const int there = min(it.klen - j * kKeys, kKeys);  // keys of the tile that exist (one at least)
-                    // a piece of 16 bytes is of key u / 8 (the swizzle moves pieces inside a row of 128 bytes only);
-                    // exponents of all ones carry into the sign bit
-                    constexpr uint32_t kExp = Half<T>::kExp, kOne = kExp == 0x7C007C00u ? 0x04000400u : 0x00800080u;
+                    // a piece of 16 bytes is of key u / 8 (the swizzle moves pieces inside a row of 128 bytes only)
                     uint32_t odd = 0;
 #pragma unroll 1
                     for (int c = 0; c < Shape::kChunks; c++) {
@@ -487,14 +487,24 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                                          : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
                                          : "r"(chunk + u * 16));
 #pragma unroll
-                            for (int w = 0; w < 4; w++) odd |= (x[w] & kExp) + kOne;
+                            for (int w = 0; w < 4; w++) odd |= not_finite<T>(x[w]);
                         }
                         for (int u = there * 8 + lane; u < kKeys * 8; u += 32)
                             asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(chunk + u * 16), "r"(0) : "memory");
                     }
                     // For each query tile that these values are multiplied with, and no other: that one's softmax warps may
                     // be past this item.  (At most two items ahead of a softmax warp.)
-                    if (odd & 0x80008000u) {
+                    if (odd) {  // this lane's pieces once more (rolled up: a longer loop here cost short prompts 0.4 us)
+#pragma unroll 1
+                        for (uint32_t at = tile + lane * 16, c = 0; c < Shape::kChunks; c++, at = tile + c * Shape::kChunk + lane * 16)
+#pragma unroll 1
+                            for (; at < tile + c * Shape::kChunk + there * 128; at += 512) {
+                                uint32_t x[4];
+                                asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]) : "r"(at));
+#pragma unroll
+                                for (int w = 0; w < 4; w++) x[w] &= ~__vcmpeq2(x[w] & Half<T>::kExp, Half<T>::kExp);
+                                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]) : "memory");
+                            }
                         if (j < n0) special[n_item % 4] = n_item + 1;
                         if (j < n1) special[4 + n_item % 4] = n_item + 1;
                     }
@@ -689,9 +699,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                 __syncwarp();
                 if (lane == 0) bar_arrive(o_empty + 8 * t);
                 // (this tile's values have all been looked over before its output was complete)
-                if (*static_cast<volatile int *>(&special[t * 4 + n_item % 4]) == n_item + 1)
-                    for (int r = it.row0 + warp * 32; r < min(it.row0 + warp * 32 + 32, it.qlen); r++)
-                        row_by_row<T, D>(a, it.head, static_cast<int64_t>(it.q0) + r, it.k0, max(r + it.offset + 1, 0));
+                if (*static_cast<volatile int *>(&special[t * 4 + n_item % 4]) == n_item + 1 && it.row0 + warp * 32 < it.qlen)
+                    add_not_finite<T, D>(a, it.head, static_cast<int64_t>(it.q0) + min(row, it.qlen - 1), it.k0, it.masked_from<kKeys>() * kKeys,
+                                         min(it.row0 + warp * 32 + 31, it.qlen - 1) + it.offset + 1, row < it.qlen, last);
             }
             steps += nt;
             outputs += nt > 0;
